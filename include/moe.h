@@ -258,6 +258,133 @@ MOE_API moe_status moe_balance(const moe_config* cfg, const float* logits, const
                                int32_t* set_load, float* bias, float gamma, void* ws,
                                moe_stream_t stream);
 
+/* The balance loss of a routed batch with its gradient ("Основы MoE", "Вспомогательный лосс
+ * Switch Transformer"), for a training step's router:
+ *   loss [1]   alpha * E * sum_i f_i P_i over the T tokens whose token_mask is not 0, with f_i
+ *              = counts_i / (T k) and P_i the mean router probability (softmax, or sigmoid
+ *              affinities normalised to sum 1, as in moe_balance); 0 when T is 0
+ *   counts [E] assignments per expert of those tokens (int32)
+ *   P [E]      mean router probability
+ *   dlogits [N][E] gradient of g * loss with respect to the logits, f held constant:
+ *              g alpha E / T * p_ti u_ti (f_i - sum_j f_j p_tj), u = 1 (softmax) or
+ *              1 - sigma(z_ti) (sigmoid); zero rows for the tokens that are masked out
+ *   grad_loss [1] device fp32 or NULL: g, the gradient of the loss (NULL: 1)
+ *   logits [N][E] fp32, ids [N][k], token_mask [N] uint8 or NULL (every token counts)
+ * Any of loss, counts, P and dlogits may be NULL.  Logits and ids of masked tokens are not used
+ * (they may hold anything).  An id outside [0, E) counts nowhere and is reported as
+ * MOE_ERR_INVALID_INPUT by moe_check_status; an id listed twice counts twice.  A token whose
+ * logits are all -infinity has no probabilities and a zero gradient, and still counts in T.
+ * A NaN logit makes the token's gradient row, P and the loss NaN.  The results depend on the
+ * inputs alone, not on the order of execution. */
+MOE_API moe_status moe_balance_loss(const moe_config* cfg, const float* logits,
+                                    const int32_t* ids, const uint8_t* token_mask, float alpha,
+                                    const float* grad_loss, float* loss, int32_t* counts,
+                                    float* P, float* dlogits, void* ws, moe_stream_t stream);
+
+/* The gradient alone, for a backward pass: dlogits as in moe_balance_loss, written
+ * (accumulate = 0) or added to what dlogits holds (accumulate = 1: the router's gradient from
+ * the gates, say; the rows of masked tokens are then left as they are). */
+MOE_API moe_status moe_balance_loss_backward(const moe_config* cfg, const float* logits,
+                                             const int32_t* ids, const uint8_t* token_mask,
+                                             float alpha, const float* grad_loss, float* dlogits,
+                                             int32_t accumulate, void* ws, moe_stream_t stream);
+
+/* ---- the row that the router and the experts read --------------------------------------
+ * RMS norm with the residual's addition and, on request, an 8-bit output with scales (the layer
+ * itself has neither; this is the step before it):
+ *   s = x + residual (fp32);  residual_out = s
+ *   y = s * rsqrt(mean(s^2) + eps) * weight
+ *   y8_scale = amax(|y|) / 448 per group of columns,  y8 = e4m3(y / y8_scale)
+ *   x, residual, residual_out, y [N][d], weight [d]: all of dtype (moe_dtype)
+ *   residual NULL: none (residual_out must be NULL too); weight NULL: ones
+ *   y8 [N][d] e4m3 bytes and y8_scale [N][ceil(d / 128)] (group = 128: every 128 columns, the
+ *   last group may be shorter) or [N][1] (group = 0: one scale for a row), fp32
+ * Any of y, residual_out and y8 with y8_scale may be NULL, but not all.  The norm takes the fp32
+ * sum, not the stored one, and the 8-bit values the fp32 y; each output is rounded once.  A
+ * group of zeros has scale 0; a scale is otherwise at least 2^-126.  A NaN or infinity in a
+ * group makes its scale non-finite.  y may be x and residual_out may be residual (the same
+ * buffer); no other overlap.  d a multiple of 8 (bf16, at most 32768) or 4 (fp32, at most
+ * 16384); eps >= 0. */
+MOE_API moe_status moe_rms_norm(int64_t N, int32_t d, int32_t dtype, const void* x,
+                                const void* residual, const void* weight, float eps, void* y,
+                                void* residual_out, void* y8, float* y8_scale, int32_t group,
+                                moe_stream_t stream);
+
+/* ---- experts with 4-bit weights ---------------------------------------------------------
+ * A decode step is bound by the bytes of the experts it reaches; in 4 bits they are a quarter.
+ * A weight is (code - 8) * scale, code 0..15, with one bf16 scale per row and group of 32, 64 or
+ * 128 consecutive columns.
+ *
+ * Storage of one rows x cols matrix (rows = outputs, cols = K), zero-padded to whole blocks:
+ *   q      [ceil(rows/16)][ceil(cols/64)][512] bytes: blocks of 16 rows x 64 columns.  With g in
+ *          0..7, t in 0..3, h, j, e, p in 0..1, byte 16 (4 g + t) + 4 (2 h + j) + 2 e + p of a
+ *          block holds the codes of its column 32 h + 8 t + 4 j + 2 p + e: row g in the low four
+ *          bits, row g + 8 in the high four.  Padding has code 8.
+ *   scale  [ceil(rows/16)][ceil(cols/group)][8][2] bf16: element (g, r) is the scale of the
+ *          block's row g + 8 r.
+ * The arrays hold mats x parts such matrices, one after another; parts = 2 is the gate and the
+ * up projection (in this order) of a SwiGLU expert. */
+typedef struct {
+  const void* q;      /* device, 16-byte aligned */
+  const void* scale;  /* device, 16-byte aligned */
+  int32_t mats;       /* experts (routed, then the shared one) */
+  int32_t parts;      /* 1 or 2 */
+  int32_t rows;       /* outputs of one part */
+  int32_t cols;       /* inputs, a multiple of 8 */
+  int32_t group;      /* columns per scale: 32, 64 or 128 */
+} moe_w4;
+
+/* Bytes of w's q (and, where scale_bytes is not NULL, of its scale); 0 on a bad shape.  Host
+ * only; the pointers in w are not read. */
+MOE_API size_t moe_w4_size(const moe_w4* w, size_t* scale_bytes);
+
+/* Codes and scales of bf16 weights W [mats][parts * rows][cols] (the layer's own W_gu and W_down
+ * layouts), written to w->q and w->scale: scale = bf16(amax / 7) of the group, code = the
+ * nearest whole number to W / scale, kept in -8..7, plus 8.  A group of zeros has scale 0; a
+ * group with a NaN has a NaN scale. */
+MOE_API moe_status moe_w4_quantize(const moe_w4* w, const void* W, moe_stream_t stream);
+
+/* out[r] = W_e x[r] for the rows r of each group (parts = 1), or SiLU(clamp(gate_e x[r])) *
+ * clamp(up_e x[r]) (parts = 2).  Products are exact and sums are fp32; out is rounded once.
+ *   x        bf16 [x_rows][cols], or with x_scale e4m3 [x_rows][cols]: x_scale fp32
+ *            [x_rows][ceil(cols / 128)] (x_group = 128) or [x_rows][1] (x_group = 0), the two
+ *            8-bit outputs of moe_rms_norm
+ *   offsets  [mats + 1] device int32: group e is rows [offsets[e], offsets[e+1]) of out, through
+ *            matrix e; NULL (mats = 1 only): all rows are one group
+ *   row_index [rows] device int32 or NULL: out row r reads x row row_index[r] (NULL: r)
+ *   rows     rows of out; those outside the groups are left untouched
+ *   out      [rows][w->rows], out_dtype MOE_DT_BF16 or MOE_DT_F32
+ *   ws       NULL, or a workspace whose status word records offsets or row indices out of range
+ *            (MOE_ERR_INVALID_INPUT; such a group is skipped, such a row reads zeros)
+ * Meant for decode: weights are read once for every 32 rows of a group. */
+MOE_API moe_status moe_w4_matmul(const moe_w4* w, const void* x, const float* x_scale,
+                                 int32_t x_group, int64_t x_rows, const int32_t* offsets,
+                                 const int32_t* row_index, int64_t rows, float clamp, void* out,
+                                 int32_t out_dtype, void* ws, moe_stream_t stream);
+
+/* moe_expert_ffn with 4-bit weights (bf16 layers): ye[r] = FFN_e(x[row_token[r]]) for r in
+ * [offsets[e], offsets[e+1]), and ye[N*k + t] = FFN_shared(x[t]) when n_shared == 1.
+ *   x [N][d] bf16, or e4m3 with x_scale [N][ceil(d / 128)] (moe_rms_norm's, group 128)
+ *   offsets [E+1], row_token [N*k]: as written by moe_permute (no gathered rows are needed)
+ *   W_gu: mats = E + S, parts = 2 (SwiGLU) or 1 (ReLU), rows = F, cols = d
+ *   W_down: mats = E + S, parts = 1, rows = d, cols = F
+ *   ye [N*k + S*N][d] bf16.  Hidden activations are rounded to bf16 in the workspace, as in
+ *   moe_expert_ffn. */
+MOE_API moe_status moe_expert_ffn_w4(const moe_config* cfg, const void* x, const float* x_scale,
+                                     const int32_t* offsets, const int32_t* row_token,
+                                     const moe_w4* W_gu, const moe_w4* W_down, void* ye, void* ws,
+                                     moe_stream_t stream);
+
+/* moe_forward with 4-bit expert weights (bf16 layers): the router reads x; the experts read x,
+ * or x8 with x8_scale (the 8-bit form of the same rows, moe_rms_norm's with group 128) when they
+ * are not NULL.  Other arguments and outputs as in moe_forward. */
+MOE_API moe_status moe_forward_w4(const moe_config* cfg, const void* x, const void* x8,
+                                  const float* x8_scale, const void* W_g,
+                                  const float* logit_offset, const float* bias,
+                                  const uint8_t* modality, const moe_w4* W_gu,
+                                  const moe_w4* W_down, void* y, const moe_route_out* route_out,
+                                  void* ws, moe_stream_t stream);
+
 /* The padded dispatch buffer [E][C][d] of "Mixture-of-Experts : routage et capacité"
  * ("Support visuel — Capacité": capacity as a tensor dimension): slot c of expert e holds the
  * c-th kept token of e in token order; empty slots are zero rows (row_token_pad = -1).  This is

@@ -22,7 +22,9 @@ _NATIVE_NAMES = {
     "config_from_shape", "MoeError", "lib", "EXPORTED", "moe_ep_first_expert", "moe_ep_plan",
     "moe_ep_workspace_size", "alloc_ep_workspace", "moe_permute_ep", "moe_ep_expert_ffn",
     "moe_ep_combine", "moe_ep_copy_runs", "moe_permute_ep_p2p", "moe_ep_combine_p2p",
-    "ipc_handle", "ipc_open", "ipc_close",
+    "ipc_handle", "ipc_open", "ipc_close", "moe_balance_loss", "moe_balance_loss_backward",
+    "moe_rms_norm", "moe_w4", "moe_w4_matmul", "moe_expert_ffn_w4",
+    "moe_forward_w4", "W4Matrix",
 }
 
 

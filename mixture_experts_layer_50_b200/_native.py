@@ -99,6 +99,22 @@ lib.moe_ep_combine_p2p.argtypes = [_cfgp] + [_vp] * 10
 lib.moe_ipc_handle.argtypes = [_vp, _vp, ctypes.POINTER(_i64)]
 lib.moe_ipc_open.argtypes = [_vp, ctypes.POINTER(_vp)]
 lib.moe_ipc_close.argtypes = [_vp]
+class moe_w4(ctypes.Structure):
+    _fields_ = [("q", _vp), ("scale", _vp), ("mats", _i32), ("parts", _i32), ("rows", _i32),
+                ("cols", _i32), ("group", _i32)]
+
+
+_w4p = ctypes.POINTER(moe_w4)
+_f32 = ctypes.c_float
+lib.moe_balance_loss.argtypes = [_cfgp] + [_vp] * 3 + [_f32] + [_vp] * 7
+lib.moe_balance_loss_backward.argtypes = [_cfgp] + [_vp] * 3 + [_f32] + [_vp] * 2 + [_i32] + [_vp] * 2
+lib.moe_rms_norm.argtypes = [_i64, _i32, _i32] + [_vp] * 3 + [_f32] + [_vp] * 4 + [_i32, _vp]
+lib.moe_w4_size.argtypes = [_w4p, ctypes.POINTER(_sz)]
+lib.moe_w4_size.restype = _sz
+lib.moe_w4_quantize.argtypes = [_w4p, _vp, _vp]
+lib.moe_w4_matmul.argtypes = [_w4p, _vp, _vp, _i32, _i64, _vp, _vp, _i64, _f32, _vp, _i32, _vp, _vp]
+lib.moe_expert_ffn_w4.argtypes = [_cfgp] + [_vp] * 4 + [_w4p] * 2 + [_vp] * 3
+lib.moe_forward_w4.argtypes = [_cfgp] + [_vp] * 7 + [_w4p] * 2 + [_vp] * 4
 lib.moe_check_dispatch_host.argtypes = [_i64, _i32, _i32, _i64] + [_vp] * 8 + [_sz]
 lib.moe_check_dispatch.argtypes = [_cfgp] + [_vp] * 8
 lib.moe_profile_begin.argtypes = [_i32]
@@ -114,7 +130,9 @@ for _f in ("moe_workspace_init", "moe_route", "moe_permute", "moe_expert_ffn", "
            "moe_forward_reroute", "moe_selftest_wait_timeout", "moe_ffn_kernels", "moe_ep_plan",
            "moe_permute_ep", "moe_ep_expert_ffn", "moe_ep_combine", "moe_check_dispatch_host",
            "moe_check_dispatch", "moe_ep_copy_runs", "moe_ipc_handle", "moe_ipc_open",
-           "moe_ipc_close", "moe_permute_ep_p2p", "moe_ep_combine_p2p"):
+           "moe_ipc_close", "moe_permute_ep_p2p", "moe_ep_combine_p2p", "moe_balance_loss",
+           "moe_balance_loss_backward", "moe_rms_norm", "moe_w4_quantize", "moe_w4_matmul",
+           "moe_expert_ffn_w4", "moe_forward_w4"):
     getattr(lib, _f).restype = ctypes.c_int
 
 EXPORTED = ("moe_workspace_size", "moe_workspace_init", "moe_capacity", "moe_route",
@@ -127,7 +145,9 @@ EXPORTED = ("moe_workspace_size", "moe_workspace_init", "moe_capacity", "moe_rou
             "moe_ep_plan", "moe_ep_workspace_size", "moe_permute_ep", "moe_ep_expert_ffn",
             "moe_ep_combine", "moe_check_dispatch_host", "moe_check_dispatch",
             "moe_ep_copy_runs", "moe_ipc_handle", "moe_ipc_open", "moe_ipc_close",
-            "moe_permute_ep_p2p", "moe_ep_combine_p2p")
+            "moe_permute_ep_p2p", "moe_ep_combine_p2p", "moe_balance_loss",
+            "moe_balance_loss_backward", "moe_rms_norm", "moe_w4_size", "moe_w4_quantize",
+            "moe_w4_matmul", "moe_expert_ffn_w4", "moe_forward_w4")
 
 
 def make_config(N, d, E, k, F, n_shared=0, n_bias_sets=0, score_fn=SOFTMAX, renorm=1,
@@ -308,6 +328,164 @@ def moe_balance(cfg, *, logits, ids, modality=None, f=None, P=None, aux=None, se
                          _ptr(P), _ptr(aux), _ptr(set_load), _ptr(bias), float(gamma), _ptr(ws),
                          _stream(stream))
     _check(st, "moe_balance")
+
+
+def _typed(t, name, dtype, *shape):
+    """Pointer of an optional tensor of the current device whose type and shape are checked."""
+    if t is None:
+        return None
+    p = _ptr(t)
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise ValueError(f"{name} has dtype {t.dtype}, not {dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    return p
+
+
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
+
+
+def moe_balance_loss(cfg, *, logits, ids, token_mask=None, alpha, grad_loss=None, loss=None,
+                     counts=None, P=None, dlogits=None, ws, stream=None):
+    """The balance loss alpha E sum f P, the counts per expert, P, and the loss's gradient with
+    respect to the logits (times ``grad_loss`` [1] on the device); ``token_mask`` (uint8 [N])
+    leaves out the tokens where it is 0."""
+    N, E, k = cfg.N, cfg.E, cfg.k
+    st = lib.moe_balance_loss(
+        ctypes.byref(cfg), _typed(logits, "logits", torch.float32, N, E),
+        _typed(ids, "ids", torch.int32, N, k), _typed(token_mask, "token_mask", torch.uint8, N),
+        alpha, _typed(grad_loss, "grad_loss", torch.float32, 1),
+        _typed(loss, "loss", torch.float32, 1), _typed(counts, "counts", torch.int32, E),
+        _typed(P, "P", torch.float32, E), _typed(dlogits, "dlogits", torch.float32, N, E),
+        _ptr(ws), _stream(stream))
+    _check(st, "moe_balance_loss")
+
+
+def moe_balance_loss_backward(cfg, *, logits, ids, token_mask=None, alpha, grad_loss=None,
+                              dlogits, accumulate=False, ws, stream=None):
+    """The gradient of the balance loss alone, written to or added to ``dlogits``."""
+    N, E, k = cfg.N, cfg.E, cfg.k
+    st = lib.moe_balance_loss_backward(
+        ctypes.byref(cfg), _typed(logits, "logits", torch.float32, N, E),
+        _typed(ids, "ids", torch.int32, N, k), _typed(token_mask, "token_mask", torch.uint8, N),
+        alpha, _typed(grad_loss, "grad_loss", torch.float32, 1),
+        _typed(dlogits, "dlogits", torch.float32, N, E), int(accumulate), _ptr(ws),
+        _stream(stream))
+    _check(st, "moe_balance_loss_backward")
+
+
+def moe_rms_norm(*, x, residual=None, weight=None, eps=1e-6, y=None, residual_out=None, y8=None,
+                 y8_scale=None, group=128, stream=None):
+    """RMS norm of ``x + residual`` times ``weight``: ``y``, the sum ``residual_out``, and the
+    8-bit form ``y8`` (float8_e4m3fn or uint8) with its fp32 scales ``y8_scale`` per ``group``
+    columns (128) or per row (0)."""
+    N, d = x.shape
+    dt = x.dtype
+    if dt not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"x has dtype {dt}, not bfloat16 or float32")
+    ng = (d + 127) // 128 if group else 1
+    st = lib.moe_rms_norm(
+        N, d, BF16 if dt == torch.bfloat16 else F32, _typed(x, "x", dt, N, d),
+        _typed(residual, "residual", dt, N, d), _typed(weight, "weight", dt, d), eps,
+        _typed(y, "y", dt, N, d), _typed(residual_out, "residual_out", dt, N, d),
+        _typed(y8, "y8", _E4M3, N, d), _typed(y8_scale, "y8_scale", torch.float32, N, ng), group,
+        _stream(stream))
+    _check(st, "moe_rms_norm")
+
+
+class W4Matrix:
+    """4-bit matrices with group scales in the library's storage (include/moe.h, moe_w4): ``q``
+    uint8 [mats, parts, ceil(rows/16), ceil(cols/64), 512] and ``scale`` bfloat16 [mats, parts,
+    ceil(rows/16), ceil(cols/group), 8, 2]."""
+
+    def __init__(self, q: torch.Tensor, scale: torch.Tensor, *, rows: int, cols: int, group: int):
+        mats, parts = q.shape[:2]
+        self.q, self.scale = q, scale
+        self.mats, self.parts, self.rows, self.cols, self.group = mats, parts, rows, cols, group
+        self.c = moe_w4(None, None, mats, parts, rows, cols, group)
+        if lib.moe_w4_size(ctypes.byref(self.c), None) == 0:
+            raise MoeError(MOE_ERR_INVALID_ARG, "moe_w4_size")
+        rb = -(-rows // 16)
+        self.c.q = _typed(q, "q", torch.uint8, mats, parts, rb, -(-cols // 64), 512)
+        self.c.scale = _typed(scale, "scale", torch.bfloat16, mats, parts, rb, -(-cols // group), 8, 2)
+
+    @classmethod
+    def quantize(cls, W: torch.Tensor, parts: int = 1, group: int = 128, stream=None) -> "W4Matrix":
+        """Codes and scales of bf16 weights ``W`` [mats][parts * rows][cols]."""
+        mats, n, cols = W.shape
+        if parts not in (1, 2) or n % parts != 0 or group not in (32, 64, 128):
+            raise ValueError("parts must be 1 or 2 and divide W's rows; group 32, 64 or 128")
+        rows = n // parts
+        rb = -(-rows // 16)
+        q = torch.empty((mats, parts, rb, -(-cols // 64), 512), dtype=torch.uint8, device=W.device)
+        scale = torch.empty((mats, parts, rb, -(-cols // group), 8, 2), dtype=torch.bfloat16,
+                            device=W.device)
+        w = cls(q, scale, rows=rows, cols=cols, group=group)
+        st = lib.moe_w4_quantize(ctypes.byref(w.c), _typed(W, "W", torch.bfloat16, mats, n, cols),
+                                 _stream(stream))
+        _check(st, "moe_w4_quantize")
+        return w
+
+
+def _row_scale(x, x_scale, group):
+    """Checks 8-bit (with x_scale) or bf16 rows; returns both pointers."""
+    n, d = x.shape
+    if x_scale is None:
+        return _typed(x, "x", torch.bfloat16, n, d), None
+    ng = (d + 127) // 128 if group else 1
+    return _typed(x, "x", _E4M3, n, d), _typed(x_scale, "x_scale", torch.float32, n, ng)
+
+
+def moe_w4_matmul(w: W4Matrix, *, x, x_scale=None, x_group=128, offsets=None, row_index=None,
+                  clamp=0.0, out, ws=None, stream=None):
+    """out = x W^T through 4-bit weights (SiLU(gate) * up for parts = 2), by groups of rows."""
+    n, d = x.shape
+    if d != w.cols:
+        raise ValueError(f"x has {d} columns, the weights {w.cols}")
+    R = out.shape[0]
+    px, ps = _row_scale(x, x_scale, x_group)
+    st = lib.moe_w4_matmul(
+        ctypes.byref(w.c), px, ps, x_group, n, _typed(offsets, "offsets", torch.int32, w.mats + 1),
+        _typed(row_index, "row_index", torch.int32, R), R, clamp,
+        _typed(out, "out", (torch.bfloat16, torch.float32), R, w.rows),
+        F32 if out.dtype == torch.float32 else BF16, _ptr(ws), _stream(stream))
+    _check(st, "moe_w4_matmul")
+
+
+def moe_expert_ffn_w4(cfg, *, x, x_scale=None, offsets, row_token, W_gu: W4Matrix,
+                      W_down: W4Matrix, ye, ws, stream=None):
+    """The expert FFNs with 4-bit weights; routed row r reads x[row_token[r]]."""
+    if tuple(x.shape) != (cfg.N, cfg.d):
+        raise ValueError(f"x has shape {tuple(x.shape)}, not {(cfg.N, cfg.d)}")
+    px, ps = _row_scale(x, x_scale, 128)
+    nk = cfg.N * cfg.k
+    st = lib.moe_expert_ffn_w4(
+        ctypes.byref(cfg), px, ps, _typed(offsets, "offsets", torch.int32, cfg.E + 1),
+        _typed(row_token, "row_token", torch.int32, nk), ctypes.byref(W_gu.c),
+        ctypes.byref(W_down.c),
+        _typed(ye, "ye", torch.bfloat16, nk + cfg.n_shared * cfg.N, cfg.d), _ptr(ws),
+        _stream(stream))
+    _check(st, "moe_expert_ffn_w4")
+
+
+def moe_forward_w4(cfg, *, x, x8=None, x8_scale=None, W_g, W_gu: W4Matrix, W_down: W4Matrix, y,
+                   logit_offset=None, bias=None, modality=None, route_out: Optional[dict] = None,
+                   ws, stream=None):
+    """The layer with 4-bit expert weights (the experts read x8 where it is given)."""
+    N, d = cfg.N, cfg.d
+    ro = None
+    if route_out:
+        ro = moe_route_out(*[_ptr(route_out.get(n)) for n, _ in moe_route_out._fields_])
+    st = lib.moe_forward_w4(
+        ctypes.byref(cfg), _typed(x, "x", torch.bfloat16, N, d), _typed(x8, "x8", _E4M3, N, d),
+        _typed(x8_scale, "x8_scale", torch.float32, N, (d + 127) // 128),
+        _typed(W_g, "W_g", torch.bfloat16, cfg.E, d), _ptr(logit_offset), _ptr(bias),
+        _ptr(modality), ctypes.byref(W_gu.c), ctypes.byref(W_down.c),
+        _typed(y, "y", torch.bfloat16, N, d), ctypes.byref(ro) if ro is not None else None,
+        _ptr(ws), _stream(stream))
+    _check(st, "moe_forward_w4")
 
 
 def moe_permute_padded(cfg, *, ids, drop_mask=None, x, offsets_pad, counts, row_token_pad=None,

@@ -117,6 +117,48 @@ cudaError_t launch_balance(const float* logits, const int32_t* ids, const uint8_
                            float* f, float* P, float* aux, int32_t* set_load, float* bias,
                            float gamma, cudaStream_t stream, int* launches);
 
+// ---- balance loss with its gradient (balance_loss.cu) ----------------------------------
+// counts [E], P [E], loss [1] and dlogits [N][E] (each may be null); accumulate: dlogits +=.
+// The scratch needs no preparation.
+size_t balance_loss_scratch_bytes(int E);
+cudaError_t launch_balance_loss(const float* logits, const int32_t* ids, const uint8_t* mask,
+                                int64_t N, int E, int k, int score_fn, float alpha,
+                                const float* grad_loss, float* loss, int32_t* counts, float* P,
+                                float* dlogits, int accumulate, void* scratch, int* status,
+                                cudaStream_t stream, int* launches);
+
+// ---- residual RMS norm (norm.cu) --------------------------------------------------------
+// group: columns that share an 8-bit scale, 128 or 0 (a whole row).
+cudaError_t launch_rms_norm(int64_t N, int d, bool f32, const void* x, const void* residual,
+                            const void* weight, float eps, void* y, void* residual_out, void* y8,
+                            float* y8_scale, int group, cudaStream_t stream, int* launches);
+
+// ---- products with 4-bit weights (w4.cu) ------------------------------------------------
+struct W4Gemm {
+  const void* q;         // [groups][parts] matrices of rows x cols in the stored layout
+  const void* scale;
+  int rows, cols, parts, group;
+  const void* x;         // bf16 [x_rows][cols], or e4m3 with x_scale
+  const float* x_scale;  // null: bf16 rows
+  int x_group;           // 128: a scale per 128 columns; 0: one per row
+  int64_t x_rows;
+  const int32_t* row_index;  // input row of each routed row, or null: the row itself
+  const int32_t* offsets;    // [n_groups + 1] device, or null: one group of max_rows rows
+  int n_groups;
+  int64_t max_rows;          // rows of the routed region
+  int64_t max_group_rows;    // no routed group has more
+  int has_shared;
+  int64_t shared_rows, shared_x_row0, shared_out_row0;
+  int relu;
+  float clamp;
+  void* out;                 // [.][rows]
+  int out_f32;
+  int* status;
+};
+cudaError_t launch_w4(const W4Gemm& p, cudaStream_t stream, int* launches);
+cudaError_t launch_w4_quantize(const void* w, int64_t mats, int rows, int cols, int group, void* q,
+                               void* scale, cudaStream_t stream, int* launches);
+
 // Padded layout: offsets_pad[e] = e * C for e <= E.
 cudaError_t launch_pad_offsets(int E, int64_t C, int32_t* offsets_pad, cudaStream_t stream,
                                int* launches);

@@ -79,7 +79,7 @@ struct Ws {
   size_t status, logits, ids, gates, local_rank, tile_hist, tile_base, demand, counts, offsets,
       slot_row, row_token, drop_mask, xp, h, ye, x_stage, y_stage, x_stage2, y_stage2, balance,
       offsets_pad, logit_parts, rr_cand, rr_val, rr_drop1, rr_offer, rr_not_offer, rr_counts1,
-      rr_scratch, total;
+      rr_scratch, balance_loss, total;
 };
 
 size_t el_size(const moe_config& c) { return c.dtype == MOE_DT_BF16 ? 2 : 4; }
@@ -136,6 +136,7 @@ Ws layout(const moe_config& c) {
   w.rr_not_offer = take(Nk);
   w.rr_counts1 = take(E * 4);
   w.rr_scratch = take(3 * (E + 1) * 4);
+  w.balance_loss = take(moe::balance_loss_scratch_bytes((int)E));
   w.total = off;
   return w;
 }
@@ -746,6 +747,97 @@ moe_status forward_impl(const moe_config* cfg, const void* x, const void* W_g,
   return MOE_OK;
 }
 
+// ---- 4-bit experts ---------------------------------------------------------------------
+moe_status check_w4_shape(const moe_w4* w) {
+  if (w == nullptr) return fail(MOE_ERR_INVALID_ARG, "the 4-bit matrix is NULL");
+  if (w->mats < 1 || w->rows < 1 || w->cols < 1)
+    return fail(MOE_ERR_INVALID_ARG, "mats, rows and cols must be positive");
+  if (w->parts != 1 && w->parts != 2) return fail(MOE_ERR_INVALID_ARG, "parts must be 1 or 2");
+  if (w->group != 32 && w->group != 64 && w->group != 128)
+    return fail(MOE_ERR_INVALID_ARG, "a 4-bit group has 32, 64 or 128 columns");
+  if (w->cols % 8 != 0) return fail(MOE_ERR_UNSUPPORTED, "4-bit matrices need cols a multiple of 8");
+  if (w->mats > 1025) return fail(MOE_ERR_UNSUPPORTED, "more than 1025 4-bit matrices");
+  if (w->rows > (1 << 24) || w->cols > (1 << 24))
+    return fail(MOE_ERR_UNSUPPORTED, "rows or cols of a 4-bit matrix above 2^24");
+  return MOE_OK;
+}
+
+moe_status check_w4(const moe_w4* w, const char* name) {
+  MOE_TRY(check_w4_shape(w));
+  MOE_TRY(need(w->q, (std::string(name) + ".q").c_str()));
+  return need(w->scale, (std::string(name) + ".scale").c_str());
+}
+
+moe_status check_ffn_w4(const moe_config& c, const moe_w4* gu, const moe_w4* down) {
+  if (c.dtype != MOE_DT_BF16) return fail(MOE_ERR_UNSUPPORTED, "4-bit experts need a bf16 layer");
+  MOE_TRY(check_w4(gu, "W_gu"));
+  MOE_TRY(check_w4(down, "W_down"));
+  const int32_t G = c.E + c.n_shared;
+  if (gu->mats != G || gu->parts != (c.act == MOE_ACT_SWIGLU ? 2 : 1) || gu->rows != c.F ||
+      gu->cols != c.d)
+    return fail(MOE_ERR_INVALID_ARG, "W_gu does not have the configuration's shape");
+  if (down->mats != G || down->parts != 1 || down->rows != c.d || down->cols != c.F)
+    return fail(MOE_ERR_INVALID_ARG, "W_down does not have the configuration's shape");
+  return MOE_OK;
+}
+
+moe::W4Gemm w4_gemm(const moe_w4& w) {
+  moe::W4Gemm p{};
+  p.q = w.q;
+  p.scale = w.scale;
+  p.rows = w.rows;
+  p.cols = w.cols;
+  p.parts = w.parts;
+  p.group = w.group;
+  return p;
+}
+
+// The two products of the experts; the routed rows are read through row_token, so no gathered
+// copy of them is made.
+moe_status stage_ffn_w4(const moe_config& c, const Ws& L, void* ws, const void* x,
+                        const float* x_scale, const int32_t* offsets, const int32_t* row_token,
+                        const moe_w4& gu, const moe_w4& down, void* ye, cudaStream_t st,
+                        int* launches) {
+  if (c.N == 0) return MOE_OK;
+  const int64_t Nk = c.N * (int64_t)c.k;
+  moe::W4Gemm p = w4_gemm(gu);
+  p.x = x;
+  p.x_scale = x_scale;
+  p.x_group = 128;
+  p.x_rows = c.N;
+  p.row_index = row_token;
+  p.offsets = offsets;
+  p.n_groups = c.E;
+  p.max_rows = Nk;
+  p.max_group_rows = c.N;
+  p.has_shared = c.n_shared;
+  p.shared_rows = c.n_shared ? c.N : 0;
+  p.shared_x_row0 = 0;
+  p.shared_out_row0 = Nk;
+  p.relu = c.act == MOE_ACT_RELU;
+  p.clamp = c.clamp;
+  p.out = at<char>(ws, L.h);
+  p.status = at<int>(ws, L.status);
+  MOE_CUDA(moe::launch_w4(p, st, launches), "4-bit gate/up product");
+  prof_mark(st);
+  moe::W4Gemm r = w4_gemm(down);
+  r.x = at<char>(ws, L.h);
+  r.x_rows = Nk + c.n_shared * c.N;
+  r.offsets = offsets;
+  r.n_groups = c.E;
+  r.max_rows = Nk;
+  r.max_group_rows = c.N;
+  r.has_shared = c.n_shared;
+  r.shared_rows = p.shared_rows;
+  r.shared_x_row0 = Nk;
+  r.shared_out_row0 = Nk;
+  r.out = ye;
+  r.status = p.status;
+  MOE_CUDA(moe::launch_w4(r, st, launches), "4-bit down product");
+  prof_mark(st);
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1070,6 +1162,231 @@ moe_status moe_balance(const moe_config* cfg, const float* logits, const int32_t
                                n_sets, at<char>(ws, L.balance), f, P, aux, set_load, bias, gamma,
                                (cudaStream_t)stream, &launches),
            "balance statistics");
+  g_last_launches = launches;
+  return MOE_OK;
+}
+
+moe_status moe_balance_loss(const moe_config* cfg, const float* logits, const int32_t* ids,
+                            const uint8_t* token_mask, float alpha, const float* grad_loss,
+                            float* loss, int32_t* counts, float* P, float* dlogits, void* ws,
+                            moe_stream_t stream) {
+  NvtxRange nvtx_range("moe_balance_loss");
+  g_last_launches = 0;
+  MOE_TRY(check_cfg(cfg));
+  MOE_TRY(check_ws(cfg, ws));
+  if (cfg->N > 0 && (logits == nullptr || ids == nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "logits and ids are required");
+  if (!(alpha == alpha)) return fail(MOE_ERR_INVALID_ARG, "alpha is NaN");
+  const Ws L = layout(*cfg);
+  int launches = 0;
+  MOE_CUDA(moe::launch_balance_loss(logits, ids, token_mask, cfg->N, cfg->E, cfg->k,
+                                    cfg->score_fn, alpha, grad_loss, loss, counts, P, dlogits, 0,
+                                    at<char>(ws, L.balance_loss), at<int>(ws, L.status),
+                                    (cudaStream_t)stream, &launches),
+           "balance loss");
+  g_last_launches = launches;
+  return MOE_OK;
+}
+
+moe_status moe_balance_loss_backward(const moe_config* cfg, const float* logits,
+                                     const int32_t* ids, const uint8_t* token_mask, float alpha,
+                                     const float* grad_loss, float* dlogits, int32_t accumulate,
+                                     void* ws, moe_stream_t stream) {
+  NvtxRange nvtx_range("moe_balance_loss_backward");
+  g_last_launches = 0;
+  MOE_TRY(check_cfg(cfg));
+  MOE_TRY(check_ws(cfg, ws));
+  if (accumulate != 0 && accumulate != 1)
+    return fail(MOE_ERR_INVALID_ARG, "accumulate must be 0 or 1");
+  if (!(alpha == alpha)) return fail(MOE_ERR_INVALID_ARG, "alpha is NaN");
+  if (cfg->N == 0) return MOE_OK;
+  if (logits == nullptr || ids == nullptr || dlogits == nullptr)
+    return fail(MOE_ERR_INVALID_ARG, "logits, ids and dlogits are required");
+  const Ws L = layout(*cfg);
+  int launches = 0;
+  MOE_CUDA(moe::launch_balance_loss(logits, ids, token_mask, cfg->N, cfg->E, cfg->k,
+                                    cfg->score_fn, alpha, grad_loss, nullptr, nullptr, nullptr,
+                                    dlogits, accumulate, at<char>(ws, L.balance_loss),
+                                    at<int>(ws, L.status), (cudaStream_t)stream, &launches),
+           "balance loss gradient");
+  g_last_launches = launches;
+  return MOE_OK;
+}
+
+moe_status moe_rms_norm(int64_t N, int32_t d, int32_t dtype, const void* x, const void* residual,
+                        const void* weight, float eps, void* y, void* residual_out, void* y8,
+                        float* y8_scale, int32_t group, moe_stream_t stream) {
+  NvtxRange nvtx_range("moe_rms_norm");
+  g_last_launches = 0;
+  if (N < 0 || d < 1) return fail(MOE_ERR_INVALID_ARG, "N must be at least 0 and d at least 1");
+  if (dtype != MOE_DT_BF16 && dtype != MOE_DT_F32)
+    return fail(MOE_ERR_INVALID_ARG, "unknown dtype");
+  if (!(eps >= 0.f)) return fail(MOE_ERR_INVALID_ARG, "eps must be at least 0");
+  if (group != 0 && group != 128) return fail(MOE_ERR_INVALID_ARG, "group must be 0 or 128");
+  if (residual == nullptr && residual_out != nullptr)
+    return fail(MOE_ERR_INVALID_ARG, "residual_out without residual");
+  if ((y8 == nullptr) != (y8_scale == nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "y8 and y8_scale go together");
+  const bool f32 = dtype == MOE_DT_F32;
+  if (d % (f32 ? 4 : 8) != 0 || d > (f32 ? 16384 : 32768))
+    return fail(MOE_ERR_UNSUPPORTED,
+                "d must be a multiple of 8 up to 32768 (bf16) or of 4 up to 16384 (fp32)");
+  if (N > INT32_MAX) return fail(MOE_ERR_UNSUPPORTED, "N above 2^31 - 1");
+  if (N == 0) return MOE_OK;
+  if (y == nullptr && residual_out == nullptr && y8 == nullptr)
+    return fail(MOE_ERR_INVALID_ARG, "no output is asked for");
+  MOE_TRY(need(x, "x"));
+  if (residual != nullptr) MOE_TRY(need(residual, "residual"));
+  if (weight != nullptr) MOE_TRY(need(weight, "weight"));
+  if (y != nullptr) MOE_TRY(need(y, "y"));
+  if (residual_out != nullptr) MOE_TRY(need(residual_out, "residual_out"));
+  if (y8 != nullptr) MOE_TRY(need(y8, "y8"));
+  int launches = 0;
+  MOE_CUDA(moe::launch_rms_norm(N, d, f32, x, residual, weight, eps, y, residual_out, y8,
+                                y8_scale, group, (cudaStream_t)stream, &launches),
+           "RMS norm");
+  g_last_launches = launches;
+  return MOE_OK;
+}
+
+size_t moe_w4_size(const moe_w4* w, size_t* scale_bytes) {
+  if (check_w4_shape(w) != MOE_OK) return 0;
+  const size_t blocks = (size_t)w->mats * w->parts * ((w->rows + 15) / 16);
+  if (scale_bytes != nullptr) *scale_bytes = blocks * ((w->cols + w->group - 1) / w->group) * 32;
+  return blocks * ((w->cols + 63) / 64) * 512;
+}
+
+moe_status moe_w4_quantize(const moe_w4* w, const void* W, moe_stream_t stream) {
+  NvtxRange nvtx_range("moe_w4_quantize");
+  g_last_launches = 0;
+  MOE_TRY(check_w4(w, "w"));
+  MOE_TRY(need(W, "W"));
+  const int64_t mats = (int64_t)w->mats * w->parts;
+  if (mats * ((w->rows + 15) / 16) * ((w->cols + 127) / 128) > INT32_MAX)
+    return fail(MOE_ERR_UNSUPPORTED, "too many weights for one call");
+  int launches = 0;
+  MOE_CUDA(moe::launch_w4_quantize(W, mats, w->rows, w->cols, w->group, const_cast<void*>(w->q),
+                                   const_cast<void*>(w->scale), (cudaStream_t)stream, &launches),
+           "4-bit quantisation");
+  g_last_launches = launches;
+  return MOE_OK;
+}
+
+moe_status moe_w4_matmul(const moe_w4* w, const void* x, const float* x_scale, int32_t x_group,
+                         int64_t x_rows, const int32_t* offsets, const int32_t* row_index,
+                         int64_t rows, float clamp, void* out, int32_t out_dtype, void* ws,
+                         moe_stream_t stream) {
+  NvtxRange nvtx_range("moe_w4_matmul");
+  g_last_launches = 0;
+  MOE_TRY(check_w4(w, "w"));
+  if (rows < 0 || x_rows < 0) return fail(MOE_ERR_INVALID_ARG, "rows and x_rows must not be negative");
+  if (rows > (1 << 30) || x_rows > (1 << 30))
+    return fail(MOE_ERR_UNSUPPORTED, "more than 2^30 rows");
+  if (offsets == nullptr && w->mats != 1)
+    return fail(MOE_ERR_INVALID_ARG, "several matrices need offsets");
+  if (x_scale != nullptr && x_group != 0 && x_group != 128)
+    return fail(MOE_ERR_INVALID_ARG, "x_group must be 0 or 128");
+  if (row_index == nullptr && x_rows < rows)
+    return fail(MOE_ERR_INVALID_ARG, "x has fewer rows than out");
+  if (!(clamp == clamp)) return fail(MOE_ERR_INVALID_ARG, "clamp is NaN");
+  if (out_dtype != MOE_DT_BF16 && out_dtype != MOE_DT_F32)
+    return fail(MOE_ERR_INVALID_ARG, "unknown out_dtype");
+  if (ws != nullptr) MOE_TRY(check_ws(nullptr, ws));
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(need(x, "x"));
+  MOE_TRY(need(out, "out"));
+  moe::W4Gemm p = w4_gemm(*w);
+  p.x = x;
+  p.x_scale = x_scale;
+  p.x_group = x_group;
+  p.x_rows = x_rows;
+  p.row_index = row_index;
+  p.offsets = offsets;
+  p.n_groups = w->mats;
+  p.max_rows = rows;
+  p.max_group_rows = rows;
+  p.clamp = clamp;
+  p.out = out;
+  p.out_f32 = out_dtype == MOE_DT_F32;
+  p.status = static_cast<int*>(ws);
+  int launches = 0;
+  MOE_CUDA(moe::launch_w4(p, (cudaStream_t)stream, &launches), "4-bit product");
+  g_last_launches = launches;
+  return MOE_OK;
+}
+
+moe_status moe_expert_ffn_w4(const moe_config* cfg, const void* x, const float* x_scale,
+                             const int32_t* offsets, const int32_t* row_token,
+                             const moe_w4* W_gu, const moe_w4* W_down, void* ye, void* ws,
+                             moe_stream_t stream) {
+  NvtxRange nvtx_range("moe_expert_ffn_w4");
+  g_last_launches = 0;
+  MOE_TRY(check_cfg(cfg));
+  MOE_TRY(check_ws(cfg, ws));
+  MOE_TRY(check_ffn_w4(*cfg, W_gu, W_down));
+  if (cfg->N == 0) return MOE_OK;
+  MOE_TRY(need(x, "x"));
+  if (offsets == nullptr || row_token == nullptr)
+    return fail(MOE_ERR_INVALID_ARG, "offsets and row_token are required");
+  MOE_TRY(need(ye, "ye"));
+  int launches = 0;
+  MOE_TRY(stage_ffn_w4(*cfg, layout(*cfg), ws, x, x_scale, offsets, row_token, *W_gu, *W_down, ye,
+                       (cudaStream_t)stream, &launches));
+  g_last_launches = launches;
+  return MOE_OK;
+}
+
+moe_status moe_forward_w4(const moe_config* cfg, const void* x, const void* x8,
+                          const float* x8_scale, const void* W_g, const float* logit_offset,
+                          const float* bias, const uint8_t* modality, const moe_w4* W_gu,
+                          const moe_w4* W_down, void* y, const moe_route_out* route_out, void* ws,
+                          moe_stream_t stream) {
+  NvtxRange nvtx_range("moe_forward_w4");
+  g_last_launches = 0;
+  MOE_TRY(check_cfg(cfg));
+  MOE_TRY(check_ws(cfg, ws));
+  MOE_TRY(check_bias(cfg, bias, modality));
+  MOE_TRY(check_ffn_w4(*cfg, W_gu, W_down));
+  MOE_TRY(need(W_g, "W_g"));
+  if (cfg->N > 0) {
+    MOE_TRY(need(x, "x"));
+    MOE_TRY(need(y, "y"));
+  }
+  if ((x8 == nullptr) != (x8_scale == nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "x8 and x8_scale go together");
+  if (x8 != nullptr) MOE_TRY(need(x8, "x8"));
+  const moe_config& c = *cfg;
+  const Ws L = layout(c);
+  const cudaStream_t st = (cudaStream_t)stream;
+  const moe_route_out none{};
+  const moe_route_out& ro = route_out != nullptr ? *route_out : none;
+  auto pick = [&](auto* user, size_t off) {
+    using T = std::remove_pointer_t<decltype(user)>;
+    return user != nullptr ? user : at<T>(ws, off);
+  };
+  float* logits = pick(ro.logits, L.logits);
+  int32_t* ids = pick(ro.ids, L.ids);
+  float* gates = pick(ro.gates, L.gates);
+  int32_t* counts = pick(ro.counts, L.counts);
+  int32_t* demand = pick(ro.demand, L.demand);
+  uint8_t* drop = pick(ro.drop_mask, L.drop_mask);
+  int32_t* offsets = pick(ro.offsets, L.offsets);
+  int32_t* slot_row = at<int32_t>(ws, L.slot_row);
+  int32_t* row_token = at<int32_t>(ws, L.row_token);
+  void* ye = at<char>(ws, L.ye);
+  int launches = 0;
+  LogitSrc zsrc;
+  MOE_TRY(stage_logits(c, L, ws, x, W_g, logit_offset, logits, at<int>(ws, L.status), st,
+                       &launches, &zsrc));
+  MOE_TRY(stage_route(c, zsrc, bias, modality, ids, gates, at<int>(ws, L.status), st, &launches));
+  MOE_TRY(stage_dispatch(c, L, ws, ids, nullptr, c.capacity, demand, counts, offsets, slot_row,
+                         row_token, drop, nullptr, nullptr, st, &launches));
+  if (debug_checks())
+    MOE_TRY(check_dispatch_device(c, ids, drop, counts, demand, offsets, slot_row, row_token,
+                                  c.capacity, st));
+  MOE_TRY(stage_ffn_w4(c, L, ws, x8 != nullptr ? x8 : x, x8 != nullptr ? x8_scale : nullptr,
+                       offsets, row_token, *W_gu, *W_down, ye, st, &launches));
+  MOE_TRY(stage_combine(c, ye, slot_row, gates, y, st, &launches));
   g_last_launches = launches;
   return MOE_OK;
 }
