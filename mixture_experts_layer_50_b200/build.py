@@ -19,7 +19,7 @@ LIB = os.path.join(HERE, "libmoe_b200.so")
 SOURCES = ["moe_api.cu", "route.cu", "dispatch.cu", "combine.cu", "gemm_tc.cu", "simt_f32.cu",
            "reroute.cu", "balance.cu", "ep_plan.cu", "ep_p2p.cu", "layout_check.cu",
            "balance_loss.cu", "norm.cu", "w4.cu"]
-HEADERS = ["common.cuh", "kernels.h"]
+HEADERS = ["common.cuh", "kernels.h", "mbar.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

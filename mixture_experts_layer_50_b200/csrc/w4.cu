@@ -8,32 +8,52 @@
 // Bound: HBM reads of the weights, half a byte each.  An SM has to take about 24 bytes, 49
 // weights, per clock, so the cost per weight of turning codes into operands decides.  The
 // matrices are stored in the order in which mma.sync reads its operand (include/moe.h): a lane's
-// 16 bytes are four A fragments of m16n8k16, every 32-bit word one of them, whose codes two
-// instructions turn into a register of two operands: (w >> 4i) & 0x000f000f | 0x4300 in each
-// half is the bf16 number 128 + code, and subtracting 136 leaves code - 8, exactly.  The
-// products with bf16 rows are exact in the fp32 accumulators; a group's sum is multiplied by
+// 16 bytes are four A fragments of m16n8k16, every 32-bit word one of them, and masks alone make
+// operands of it.  A code in the low bits of a 16-bit float, all else zero, is a subnormal number:
+// code * 2^-133 in bf16 (2^-24 in fp16), and 16 times that where the code lies four bits higher
+// (the step from the subnormal to the first normal numbers is even, so bf16's seven bits of
+// mantissa suffice).  w & 0x000f000f is the fragment's rows g, w & 0x00f000f0 its rows g + 8, and
+// w >> 8 has the other columns of both: five instructions for eight weights.  The 8 that every
+// code is too large by is -8 sum(x) over a group of columns, the same for all weights: it is made
+// once, where the rows arrive, and is what the group's sums start from.  The powers of two go
+// into the result at the end.  To keep bf16 products out of fp32's own subnormal range, the rows
+// are multiplied by 2^64 as they arrive in shared memory; so a row's numbers count as infinite
+// from 2^63 on.
+// The products with bf16 rows are exact in the fp32 accumulators; a group's sum is multiplied by
 // its scale in fp32.  8-bit rows (e4m3 with scales) are widened to fp16, also exactly, and their
 // scales join the weights' scales on the sums.  Nothing is rounded below 32 bits before the
 // output.
 //
-// A warp owns 32 output rows (two blocks of 16; for SwiGLU a gate block and its up block) and
-// all rows of one tile of a group: weights go from HBM to registers, kDepth steps of 128
-// columns ahead, and straight into the tensor cores; the few activation rows come from L1.
-// There is no barrier in the loop and none between warps unless the columns are split among
-// the kSplit warps of an item, which small problems do to have enough loads in flight; the
-// partial sums then meet in shared memory and are added in order.
+// A block of warps owns one tile of a group's rows (up to 32) and 32 output rows for every warp,
+// two blocks of 16 (for SwiGLU a gate block and its up block).  Every warp
+// runs a ring of its own in shared memory for the weights that it alone needs: each lane copies
+// asynchronously what that lane will read, kDepth steps of 256 columns ahead and on across
+// items, without a barrier.  The activation rows, which all warps need, come in chunks of
+// several steps into three buffers: every warp copies its part of a chunk two chunks ahead and
+// makes operands of it one chunk ahead, and mbarriers tell when all have, so the warps may run
+// apart by most of a chunk.  The items are dealt to the resident blocks in whole rounds; those
+// that are left, or all where there are few, are cut into 2, 4, 8 or 16
+// units, whichever ends first, whose warps share out the columns of fewer output rows.  Their
+// partial sums meet in shared memory and are added in order.
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <algorithm>
+#include <climits>
+
+#include <atomic>
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
+#include "mbar.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kDepth = 2;         // steps of 128 columns in flight per warp
+namespace cg = cooperative_groups;
+
 constexpr int kMaxGroups = 1025;  // 1024 routed groups and the shared one
 
 struct Args {
@@ -47,102 +67,172 @@ struct Args {
   const int32_t* row_index;
   const int32_t* offsets;
   int n_groups, has_shared;
-  int64_t max_rows, shared_rows, shared_x_row0, shared_out_row0;
-  int items_per_tile, split, act;
+  int64_t max_rows, max_group_rows, shared_rows, shared_x_row0, shared_out_row0;
+  int pairs, max_split, buf_bytes, cluster, relu;
   float clamp;
   void* out;
   int out_f32;
   int* status;
 };
 
-__device__ __forceinline__ uint4 ldg_stream(const uint4* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+// Warps of a block, as many as the registers allow (one block on an SM), and the steps of 256
+// columns in a warp's ring, of two blocks' weights and scales each.
+constexpr int kWarps = 16, kThreads = 32 * kWarps, kDepth = 2;
+constexpr int kDynamicSmem = 220 * 1024;  // of 227 KB, less the tables
+constexpr int kStepQ = 4096, kStep = kStepQ + 512;
+constexpr int kBuffers = 3;  // of input rows
+
+// Input rows in shared memory are 16-bit operands, with a pad that keeps the fragments' reads
+// free of bank conflicts.  A buffer is the rows, then for every group of columns -8 sum(x) of
+// each row, then (8-bit rows) the scales of each 128 columns and row.
+__host__ __device__ constexpr int x_pitch(int steps) { return 512 * steps + 64; }
+__host__ __device__ constexpr int x_bytes(bool x8, int tile, int rows, int steps, int group) {
+  return (rows * x_pitch(steps) + tile * 4 * steps * (256 / group + (x8 ? 2 : 0)) + 15) / 16 * 16;
+}
+// Steps that a buffer has room for (16 at most: a warp copies the scales of a chunk at once).
+__host__ __device__ constexpr int x_steps_of(int bytes, bool x8, int tile, int rows, int group) {
+  const int n = (bytes - 64 * rows) / (512 * rows + tile * 4 * (256 / group + (x8 ? 2 : 0)));
+  return n < 16 ? n : 16;
+}
+// Bytes of the partial sums: of the warps of units cut into `split`, or of a run of pairs that
+// the blocks of a cluster hand over at once.
+constexpr int kHandOver = 8;
+__host__ __device__ constexpr int sum_bytes(int nt, int split, int cluster) {
+  const int pairs = kWarps - kWarps / split;
+  return (cluster > 1 && pairs < kHandOver ? kHandOver : pairs) * 8 * nt * 32 * 4;
 }
 
-template <bool kHalf>
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                    uint32_t b1, bool zero) {
-  const float c0 = zero ? 0.f : d[0], c1 = zero ? 0.f : d[1], c2 = zero ? 0.f : d[2],
-              c3 = zero ? 0.f : d[3];
-  if constexpr (kHalf)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%10,%11,%12,%13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1),
-          "f"(c2), "f"(c3));
+// What `rest` items take on n blocks (or clusters) when each is cut into 2^cut units, in half
+// steps: the rounds of units times the unit's steps and half a step beside them.
+__host__ __device__ __forceinline__ int64_t cost_of(int64_t rest, int n, int steps, int cut) {
+  return ((rest << cut) + n - 1) / n * (((steps + (1 << cut) - 1) >> cut) * 2 + 1);
+}
+
+// Asynchronous copies to shared memory.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// Eight columns of an input row on their way into a slot of 16 bytes (8-bit rows, which start on
+// 8 bytes, into its upper half).
+template <bool kX8>
+__device__ __forceinline__ void copy_x(uint32_t slot, const void* src) {
+  if constexpr (kX8)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(slot + 8), "l"(src) : "memory");
   else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%10,%11,%12,%13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1),
-          "f"(c2), "f"(c3));
+    copy16(slot, src);
 }
-
-// The four A registers of one word of codes.
-template <bool kHalf>
-__device__ __forceinline__ void widen(uint32_t w, uint32_t (&a)[4]) {
-  if constexpr (kHalf) {
-    // fp16 has room for a code at bits 4-7 too: 1024 + 16 code, brought back by * 1/16 - 72
-    const __half2 k1032 = __floats2half2_rn(1032.f, 1032.f);
-    const __half2 k16 = __floats2half2_rn(0.0625f, 0.0625f), k72 = __floats2half2_rn(-72.f, -72.f);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t v = i == 0 ? w : w >> 8;
-      const uint32_t lo = (v & 0x000f000fu) | 0x64006400u, hi = (v & 0x00f000f0u) | 0x64006400u;
-      const __half2 l = __hsub2(*reinterpret_cast<const __half2*>(&lo), k1032);
-      const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&hi), k16, k72);
-      a[2 * i] = *reinterpret_cast<const uint32_t*>(&l);
-      a[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-  } else {
-    const __nv_bfloat162 k136 = __floats2bfloat162_rn(136.f, 136.f);
+// The slot's eight columns as operands: bf16 times 2^64, or fp16; returns their sum.
+template <bool kX8>
+__device__ __forceinline__ float make_x(uint32_t slot) {
+  uint32_t v[4];
+  float sum = 0.f;
+  if constexpr (kX8) {
+    uint32_t lo, hi;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(lo), "=r"(hi) : "r"(slot + 8) : "memory");
+    const uint16_t p[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-      const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), k136);
-      a[i] = *reinterpret_cast<const uint32_t*>(&r);
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(v[i]) : "h"(p[i]));
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[i]));
+      sum += f.x + f.y;
+    }
+  } else {
+    const __nv_bfloat162 k = __floats2bfloat162_rn(18446744073709551616.f, 18446744073709551616.f);
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(slot)
+                 : "memory");
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v[i]), k);
+      v[i] = *reinterpret_cast<const uint32_t*>(&r);
+      sum += __uint_as_float(v[i] << 16) + __uint_as_float(v[i] & 0xffff0000u);
     }
   }
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(slot), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3])
+               : "memory");
+  return sum;
+}
+__device__ __forceinline__ void zero_x(uint32_t slot) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(slot), "r"(0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest kLeft groups have arrived.
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// Eight columns of a row as the B registers of two mma steps.
+// d += a b
+template <bool kHalf>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                    uint32_t b1) {
+  if constexpr (kHalf)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The four A registers of one word of codes: the codes as subnormal numbers, those of rows g + 8
+// 16 times as large.
+__device__ __forceinline__ void widen(uint32_t w, uint32_t (&a)[4]) {
+  a[0] = w & 0x000f000fu;
+  a[1] = w & 0x00f000f0u;
+  a[2] = (w >> 8) & 0x000f000fu;
+  a[3] = (w >> 8) & 0x00f000f0u;
+}
+// What makes codes of them again, for rows g and rows g + 8.
 template <bool kX8>
-__device__ __forceinline__ void load_x(const void* x, int64_t at, bool ok, uint32_t (&b)[4]) {
-  if constexpr (kX8) {
-    uint2 v = make_uint2(0, 0);
-    if (ok) v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(x) + at));
-    const uint16_t p[4] = {(uint16_t)v.x, (uint16_t)(v.x >> 16), (uint16_t)v.y,
-                           (uint16_t)(v.y >> 16)};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b[i]) : "h"(p[i]));
-  } else {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (ok) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x) + at));
-    b[0] = v.x;
-    b[1] = v.y;
-    b[2] = v.z;
-    b[3] = v.w;
-  }
+__device__ __forceinline__ float code_unit(bool upper) {
+  const float u = kX8 ? 16777216.f : 590295810358705651712.f;  // 2^24, 2^(133 - 64)
+  return upper ? u * 0.0625f : u;
 }
 
 __device__ __forceinline__ float clip(float v, float c) { return v > c ? c : v < -c ? -c : v; }
 
-template <int kNt, bool kX8, int kGroup>
-__global__ void __launch_bounds__(kThreads, kNt == 4 ? 1 : 2) w4_kernel(const Args a) {
-  constexpr int kTile = 8 * kNt;       // rows of a group that one item takes
-  constexpr int kSteps = 128 / kGroup; // groups in 128 columns
-  pdl_wait();
+// A unit of work of a block.
+struct Item {
+  int e = 0, tile_rows = 0;
+  int pair0 = 0, n_pairs = 0;  // the unit's pairs of blocks of 16 rows
+  int log2 = 0, split = 1;     // warps that share the columns of a pair
+  int steps = 0;               // of 256 columns, of the longest share
+  int x_steps = 0;             // steps (of all shares together) of a chunk of input rows
+  bool shared = false;
+  int64_t in_row0 = 0, out_row0 = 0;
+};
+
+template <int kNt, bool kX8, int kGroup, bool kCluster>
+__global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
+  constexpr int kTile = 8 * kNt;        // rows of a group that one item takes
+  constexpr int kSteps = 256 / kGroup;  // groups in a step
+  constexpr int kEl = kX8 ? 1 : 2;      // bytes of an input element
   __shared__ int32_t s_first[kMaxGroups + 1];  // first tile of each group
   __shared__ int32_t s_warp[kWarps];
-  extern __shared__ float s_red[];  // [kWarps][8 kNt][32] when split
+  extern __shared__ __align__(16) char s_ring[];  // the rings, two buffers of rows
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int n_all = a.n_groups + a.has_shared;
+  __shared__ uint64_t s_full[kBuffers], s_free[kBuffers];
+  __shared__ int s_abort;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kBuffers; ++i) {
+      tc::mbar_init(&s_full[i], kWarps);
+      tc::mbar_init(&s_free[i], kWarps);
+    }
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_wait();
 
   auto group_range = [&](int e, int64_t& first, int64_t& n) {
     if (e >= a.n_groups) {
@@ -154,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, kNt == 4 ? 1 : 2) w4_kernel(const Ar
     } else {
       first = a.offsets[e];
       n = a.offsets[e + 1] - first;
-      if (first < 0 || n < 0 || first + n > a.max_rows) n = -1;
+      if (first < 0 || n < 0 || n > a.max_group_rows || first + n > a.max_rows) n = -1;
     }
   };
   {
@@ -190,16 +280,240 @@ __global__ void __launch_bounds__(kThreads, kNt == 4 ? 1 : 2) w4_kernel(const Ar
     if (threadIdx.x == kThreads - 1) s_first[n_all] = at;
     __syncthreads();
   }
-  const int64_t items = (int64_t)s_first[n_all] * a.items_per_tile;
-  const int split = a.split, slots = kWarps / split;
-  const int ks = warp % split;
-  const int n_steps = (a.ku + 1) / 2;
-  const int st0 = (int)((int64_t)n_steps * ks / split);
-  const int st1 = (int)((int64_t)n_steps * (ks + 1) / split);
+  // The blocks of a cluster work on the same items, each on its run of the steps, k0 onwards.
+  const int per = kCluster ? a.cluster : 1, all_steps = (a.ku + 3) / 4, rank = blockIdx.x % per;
+  const int k0 = all_steps * rank / per;
+  const int n_steps = all_steps * (rank + 1) / per - k0;
+  // an item: a tile and a pair of blocks for each warp; those after the last whole round of the blocks are
+  // cut into 2^cut units
+  const int chunks = (a.pairs + kWarps - 1) / kWarps;
+  const int n_blocks = (int)gridDim.x / per, block = (int)blockIdx.x / per;
+  const int items = s_first[n_all] * chunks;  // (units are below 2^31: checked on the host)
+  const int rest = items % n_blocks, whole = items - rest;
+  int cut = 0;
+  for (int c = 1; 1 << c <= a.max_split; ++c) {
+    const int most = (all_steps + per - 1) / per;  // (the cut is all blocks' alike)
+    if (cost_of(rest, n_blocks, most, c) < cost_of(rest, n_blocks, most, cut)) cut = c;
+  }
+  const int units = whole + (rest << cut);
 
-  for (int64_t it = (int64_t)blockIdx.x * slots; it < items; it += (int64_t)gridDim.x * slots) {
-    const int64_t item = it + warp / split;
-    const bool valid = item < items;
+  auto item_at = [&](int unit) {
+    Item r;
+    int it = unit, part = 0;
+    if (unit >= whole) {
+      it = whole + ((unit - whole) >> cut);
+      part = (unit - whole) & ((1 << cut) - 1);
+      r.log2 = cut;
+      r.split = 1 << cut;
+    }
+    const int tile = (int)((unsigned)it / (unsigned)chunks);
+    r.pair0 = (it - tile * chunks) * kWarps + part * (kWarps >> r.log2);
+    r.n_pairs = min(kWarps >> r.log2, a.pairs - r.pair0);
+    r.steps = (n_steps + r.split - 1) >> r.log2;
+    int hi = n_all;  // the group that owns the tile: s_first[e] <= tile < s_first[e + 1]
+    while (hi - r.e > 1) {
+      const int mid = (r.e + hi) >> 1;
+      if (s_first[mid] <= tile)
+        r.e = mid;
+      else
+        hi = mid;
+    }
+    int64_t first, n;
+    group_range(r.e, first, n);
+    const int64_t row0 = (int64_t)(tile - s_first[r.e]) * kTile;
+    r.tile_rows = (int)min((int64_t)kTile, n - row0);
+    r.x_steps = min(x_steps_of(a.buf_bytes, kX8, kTile, r.tile_rows, kGroup), n_steps + r.split - 1) >>
+                r.log2 << r.log2;
+    r.shared = r.e >= a.n_groups;
+    r.out_row0 = (r.shared ? a.shared_out_row0 : first) + row0;
+    r.in_row0 = (r.shared ? a.shared_x_row0 : first) + row0;
+    return r;
+  };
+  // the input row of a tile's row r; -1 where its index is out of range
+  auto row_of = [&](const Item& im, int r) -> int64_t {
+    int64_t v = im.in_row0 + r;
+    if (!im.shared && a.row_index != nullptr) v = a.row_index[v];
+    return v < 0 || v >= a.x_rows ? -1 : v;
+  };
+
+  // ---- input rows, in chunks ----
+  // A warp's part of a chunk, of slots of 8 columns: with the rows rounded up to a power of two,
+  // `over`, it is row warp % over, and of its runs of 32 slots every (kWarps / over)-th from
+  // warp / over.
+  char* const s_x = s_ring + kWarps * kDepth * kStep;
+  const uint32_t x0 = (uint32_t)__cvta_generic_to_shared(s_x);
+  // where a buffer's sums [group][kTile] and scales [128 columns][kTile] begin
+  auto sums_of = [](int rows, int x_steps) { return rows * x_pitch(x_steps); };
+  auto scales_of = [](int rows, int x_steps) {
+    return rows * x_pitch(x_steps) + x_steps * kSteps * kTile * 4;
+  };
+  int c_it = block;  // unit and first step of the chunk to copy next
+  int c_s = 0, c_steps = 0, c_log2 = 0, c_rows = 0, c_over = 1, c_x_steps = 0, c_buf = 0;
+  uint32_t c_phase = 0;    // of the buffer's last freeing
+  const char* c_x = nullptr;  // the warp's row at the next chunk's first column
+  const float* c_xs = nullptr;
+  int n_copied = 0;        // chunks
+  // of the two chunks copied last: rows, slots of a row, and those before the last column
+  int d_rows[2] = {0, 0}, d_over[2] = {1, 1}, d_steps[2] = {0, 0}, d_slots[2] = {0, 0}, d_inside[2] = {0, 0};
+  bool dead = false;  // a wait ran out: nothing is stored any more
+  auto copy_chunk = [&]() {
+    if (c_it >= units) return;
+    if (c_s == 0) {
+      const Item im = item_at(c_it);
+      c_steps = im.steps;
+      c_log2 = im.log2;
+      c_rows = im.tile_rows;
+      c_x_steps = im.x_steps;
+      c_over = 1 << (32 - __clz(c_rows - 1));
+      const int r = min(warp & (c_over - 1), c_rows - 1);
+      const int64_t row = max(row_of(im, r), (int64_t)0);
+      c_x = static_cast<const char*>(a.x) + (row * a.cols + 256 * k0 + 8 * lane) * kEl;
+      c_xs = kX8 ? a.x_scale + row * a.xs_ld + (2 * k0 + lane) * a.xs_step : nullptr;
+    }
+    const int st0 = c_s << c_log2, pitch = x_pitch(c_x_steps);
+    const int slots = min(c_x_steps, n_steps - st0) * 32;
+    const int inside = min(slots, (a.cols - 256 * (k0 + st0)) >> 3);
+    // every warp is done with what the buffer held
+    if (n_copied >= kBuffers && !dead)
+      dead = !tc::mbar_wait(&s_free[c_buf], c_phase, &s_abort, a.status);
+    const int r = warp & (c_over - 1);
+    if (r < c_rows) {
+      const uint32_t to = x0 + c_buf * a.buf_bytes, at = to + r * pitch + 16 * lane;
+      const int first = warp / c_over * 32, turn = kWarps / c_over * 32;
+      for (int i = first; i + lane < inside; i += turn) copy_x<kX8>(at + 16 * i, c_x + 8 * kEl * i);
+      if (kX8 && first == 0 && 16 * lane < inside)
+        copy4(to + scales_of(c_rows, c_x_steps) + (lane * kTile + r) * 4, c_xs);
+    }
+    c_x += c_x_steps * 256 * kEl;
+    if (kX8) c_xs += 2 * c_x_steps * a.xs_step;
+    d_rows[1] = d_rows[0], d_over[1] = d_over[0], d_steps[1] = d_steps[0];
+    d_slots[1] = d_slots[0], d_inside[1] = d_inside[0];
+    d_rows[0] = c_rows, d_over[0] = c_over, d_steps[0] = c_x_steps;
+    d_slots[0] = slots, d_inside[0] = inside;
+    if (++c_buf == kBuffers) {
+      c_buf = 0;
+      if (n_copied >= kBuffers) c_phase ^= 1;
+    }
+    copies_commit();  // a group of its own: whichever steps follow, the waits for theirs cover it
+    ++n_copied;
+    c_s += c_x_steps >> c_log2;
+    if (c_s >= c_steps) {
+      c_s = 0;
+      c_it += n_blocks;
+    }
+  };
+  // Operands, and sums by groups, of the warp's part of a chunk that has landed: the chunk
+  // copied last, or the one before it.
+  int m_buf = 0, n_made = 0;
+  auto make_chunk = [&]() {
+    if (n_made >= n_copied) return;
+    const bool older = n_copied - n_made == 2;
+    const int rows = older ? d_rows[1] : d_rows[0], slots = older ? d_slots[1] : d_slots[0];
+    const int inside = older ? d_inside[1] : d_inside[0], over = older ? d_over[1] : d_over[0];
+    const int x_steps = older ? d_steps[1] : d_steps[0], pitch = x_pitch(x_steps);
+    const uint32_t at = x0 + m_buf * a.buf_bytes, sums = at + sums_of(rows, x_steps);
+    constexpr int kLanes = kGroup / 8;  // slots of a group
+    const int r = warp & (over - 1);
+    if (r < rows) {
+      for (int i = warp / over * 32 + lane; i - lane < slots; i += kWarps / over * 32) {
+        float sum = 0.f;
+        if (i < inside)
+          sum = make_x<kX8>(at + r * pitch + 16 * i);
+        else if (i < slots)
+          zero_x(at + r * pitch + 16 * i);
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (i % kLanes == 0 && i < slots)
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(sums + (i / kLanes * kTile + r) * 4),
+                       "f"(sum * (kX8 ? 1.f : 5.42101086e-20f) * (-8.f / code_unit<kX8>(false)))
+                       : "memory");
+      }
+    }
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&s_full[m_buf]);
+    m_buf = m_buf + 1 == kBuffers ? 0 : m_buf + 1;
+    ++n_made;
+  };
+
+  // ---- weights: the warp's ring; step f_s of the share of unit f_it is fetched next ----
+  char* const s_mine = s_ring + warp * (kDepth * kStep);
+  const uint32_t ring0 = (uint32_t)__cvta_generic_to_shared(s_mine) + lane * 16;
+  int f_it = block;
+  int f_plain = 0;                       // steps of the share before its last one
+  int f_s = 0, f_steps = 0, f_n = 0;     // then: the step, the unit's steps, and the share's
+  int f_last = 0, f_dq = 0, f_ds = 0;    // the last step's place; bytes from a step to the next
+  const char *fq0 = nullptr, *fq1 = nullptr, *fs = nullptr;
+  const int s_m = lane >= 2 * kSteps, s_c = lane % (2 * kSteps);  // the lane's 16 bytes of scales
+  // the warp's share and pair of a unit
+  auto steps_of = [&](const Item& im) {
+    const int ks = warp & (im.split - 1);
+    return warp >> im.log2 < im.n_pairs ? (n_steps - ks + im.split - 1) >> im.log2 : 0;
+  };
+  auto fetch_item = [&]() {
+    f_plain = f_s = f_n = 0;
+    f_steps = 1;
+    if (f_it >= units) return;
+    const Item im = item_at(f_it);
+    const int ks = warp & (im.split - 1), pair = im.pair0 + (warp >> im.log2);
+    f_steps = im.steps;
+    f_n = steps_of(im);
+    f_plain = f_s = max(f_n - 1, 0);
+    f_last = k0 + f_s * im.split + ks;
+    f_dq = 2048 * im.split;
+    f_ds = 32 * kSteps * im.split;
+    const int64_t blk = (int64_t)im.e * a.parts * a.rb;
+    const int64_t b0 = blk + (a.parts == 2 ? pair : 2 * pair);
+    const int64_t b1 = blk + (a.parts == 2 ? a.rb + pair : min(2 * pair + 1, a.rb - 1));
+    fq0 = reinterpret_cast<const char*>(a.q + (b0 * a.ku + 4 * (k0 + ks)) * 32 + lane);
+    fq1 = reinterpret_cast<const char*>(a.q + (b1 * a.ku + 4 * (k0 + ks)) * 32 + lane);
+    fs = reinterpret_cast<const char*>(a.scale + ((s_m ? b1 : b0) * a.ng + (k0 + ks) * kSteps) * 8 + 4 * s_c);
+  };
+  // the next step into the ring at `at` (an empty group where there is none)
+  auto fetch = [&](int at) {
+    const uint32_t dst = ring0 + at;
+    if (f_plain > 0) {
+      --f_plain;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        copy16(dst + 512 * u, fq0 + 512 * u);
+        copy16(dst + 2048 + 512 * u, fq1 + 512 * u);
+      }
+      if (lane < 4 * kSteps) copy16(dst + kStepQ, fs);
+      fq0 += f_dq;
+      fq1 += f_dq;
+      fs += f_ds;
+    } else {
+      if (f_s < f_n) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (4 * f_last + u >= a.ku) break;  // (old codes meet zero columns there)
+          copy16(dst + 512 * u, fq0 + 512 * u);
+          copy16(dst + 2048 + 512 * u, fq1 + 512 * u);
+        }
+        if (lane < 4 * kSteps && f_last * kSteps + s_c / 2 < a.ng) copy16(dst + kStepQ, fs);
+      }
+      if (++f_s >= f_steps) {
+        f_it += n_blocks;
+        fetch_item();
+      }
+    }
+    copies_commit();
+  };
+
+  fetch_item();
+  copy_chunk();
+  fetch(0);
+  copy_chunk();
+#pragma unroll
+  for (int p = 1; p < kDepth; ++p) fetch(p * kStep);
+  copies_wait<kDepth - 1>();  // the first chunk
+  make_chunk();
+  int buf = 0, at = 0;
+  uint32_t x_phase = 0;
+  for (int unit = block; unit < units; unit += n_blocks) {
+    const Item im = item_at(unit);
+    const int ks = warp & (im.split - 1), pair = im.pair0 + (warp >> im.log2);
+    const int n_mine = steps_of(im), chunk = im.x_steps >> im.log2;
     float acc[2][kNt][4];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -207,179 +521,149 @@ __global__ void __launch_bounds__(kThreads, kNt == 4 ? 1 : 2) w4_kernel(const Ar
       for (int n = 0; n < kNt; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
-    int e = 0, pair = 0, n_act = 0, tile_rows = 0;
-    int64_t out_row0 = 0;
-    if (valid) {
-      const int tile = (int)(item / a.items_per_tile);
-      pair = (int)(item % a.items_per_tile);
-      int hi = n_all;  // the group that owns the tile: s_first[e] <= tile < s_first[e + 1]
-      while (hi - e > 1) {
-        const int mid = (e + hi) >> 1;
-        if (s_first[mid] <= tile)
-          e = mid;
-        else
-          hi = mid;
-      }
-      int64_t first, n;
-      group_range(e, first, n);
-      const int64_t row0 = (int64_t)(tile - s_first[e]) * kTile;
-      tile_rows = (int)min((int64_t)kTile, n - row0);
-      n_act = (tile_rows + 7) / 8;
-      const bool shared = e >= a.n_groups;
-      out_row0 = (shared ? a.shared_out_row0 : first) + row0;
-      const int64_t in_row0 = (shared ? a.shared_x_row0 : first) + row0;
-
-      // the input rows this lane reads, and those whose sums it holds
-      int64_t x_at[kNt];
-      int32_t xs_at[kNt][2];
-      auto row_of = [&](int r) -> int64_t {
-        if (r >= tile_rows) return -1;
-        int64_t v = in_row0 + r;
-        if (!shared && a.row_index != nullptr) v = a.row_index[v];
-        if (v < 0 || v >= a.x_rows) {
-          report_status(a.status, kStatusInvalidInput);
-          return -1;
-        }
-        return v;
-      };
+    // the item's steps with kN blocks of 8 rows
+    auto steps = [&](auto blocks) {
+      constexpr int kN = decltype(blocks)::value;
+      // What a column of an mma holds depends on its own row alone: rows behind the tile's last
+      // one read that one again, and their sums are not stored.
+      int x_off[kN];
 #pragma unroll
-      for (int n = 0; n < kNt; ++n) {
-        const int64_t r = row_of(8 * n + g);
-        x_at[n] = r < 0 ? -1 : r * a.cols;
-        if (kX8) {
+      for (int n = 0; n < kN; ++n)
+        x_off[n] = min(8 * n + g, im.tile_rows - 1) * x_pitch(im.x_steps) + 16 * t;
+      for (int c0 = 0; c0 < im.steps; c0 += chunk) {
+        if (!dead) dead = !tc::mbar_wait(&s_full[buf], x_phase, &s_abort, a.status);
+        const int n_now = dead ? 0 : n_mine, end = min(c0 + chunk, im.steps);
+        const char* px = s_x + buf * a.buf_bytes + ks * 512;
+        const char* po = s_x + buf * a.buf_bytes + sums_of(im.tile_rows, im.x_steps) +
+                         (ks * kSteps * kTile + 2 * t) * 4;
+        const char* pxs = s_x + buf * a.buf_bytes + scales_of(im.tile_rows, im.x_steps) +
+                          (2 * ks * kTile + 2 * t) * 4;
+        // a first step, to let the other warps end the chunk before; then the next chunk but one
+        // is copied (and where a chunk is short, the next one made), and the other steps follow
+        int s = c0;
+        bool copied = false;
+        for (int stop = c0 + 1;; stop = end) {
+        for (; s < stop; ++s) {
+          copies_wait<kDepth - 1>();
+          __syncwarp();  // other lanes' scales
+          if (s < n_now) {
+            const char* pq = s_mine + at + lane * 16;
+            const uint32_t* ps = reinterpret_cast<const uint32_t*>(s_mine + at + kStepQ) + g;
+            // of the step's groups, the last there is
+            const int st = k0 + (s << im.log2) + ks, g_last = a.ng - 1 - st * kSteps;
+            float part[2][kN][4];
+            uint4 w[2];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int64_t rr = row_of(8 * n + 2 * t + i);
-            xs_at[n][i] = rr < 0 ? -1 : (int32_t)rr;
-          }
-        }
-      }
-      // the item's two blocks of 16 rows
-      int b0, b1;
-      if (a.parts == 2) {
-        b0 = pair;
-        b1 = a.rb + pair;
-      } else {
-        b0 = 2 * pair;
-        b1 = min(b0 + 1, a.rb - 1);
-      }
-      const int64_t blk = (int64_t)e * a.parts * a.rb;
-      const uint4* q0 = a.q + (blk + b0) * a.ku * 32 + lane;
-      const uint4* q1 = a.q + (blk + b1) * a.ku * 32 + lane;
-      const uint32_t* sc0 = a.scale + (blk + b0) * a.ng * 8;
-      const uint32_t* sc1 = a.scale + (blk + b1) * a.ng * 8;
-
-      uint4 wq[kDepth][2][2];
-      uint32_t ws[kDepth][2];
-      auto fetch = [&](uint4 (&w)[2][2], uint32_t (&s)[2], int st) {
-        const int u = 2 * st;
-        const uint4 none = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-        w[0][0] = ldg_stream(q0 + (int64_t)u * 32);
-        w[0][1] = ldg_stream(q1 + (int64_t)u * 32);
-        if (u + 1 < a.ku) {
-          w[1][0] = ldg_stream(q0 + (int64_t)(u + 1) * 32);
-          w[1][1] = ldg_stream(q1 + (int64_t)(u + 1) * 32);
-        } else {
-          w[1][0] = w[1][1] = none;
-        }
-        // one word is the scales of rows g and g + 8; lane 8 i + j fetches word j of the i-th
-        // group of the step (one group: every lane its own)
-        const int gi = kSteps == 1 ? st : min(st * kSteps + (lane >> 3) % kSteps, a.ng - 1);
-        const int wi = gi * 8 + (kSteps == 1 ? g : (lane & 7));
-        s[0] = __ldg(sc0 + wi);
-        s[1] = __ldg(sc1 + wi);
-      };
+            for (int h = 0; h < 8; ++h) {  // 32 columns each
+              if (h == 4 && 256 * st + 128 >= a.cols) break;
+              if (h % 2 == 0) {
+                w[0] = *reinterpret_cast<const uint4*>(pq + 256 * h);
+                w[1] = *reinterpret_cast<const uint4*>(pq + 256 * h + 2048);
+              }
+              uint4 b[kN];
 #pragma unroll
-      for (int p = 0; p < kDepth; ++p)
-        if (st0 + p < st1) fetch(wq[p], ws[p], st0 + p);
-
-      for (int s0 = st0; s0 < st1; s0 += kDepth) {
+              for (int n = 0; n < kN; ++n)
+                b[n] = *reinterpret_cast<const uint4*>(px + x_off[n] + 64 * h);
+              if (h % (kGroup / 32) == 0) {
 #pragma unroll
-        for (int p = 0; p < kDepth; ++p) {
-          const int st = s0 + p;
-          if (st >= st1) break;
-          uint4 w[2][2];
-          uint32_t sw[2];
+                for (int n = 0; n < kN; ++n) {
+                  const float2 o = *reinterpret_cast<const float2*>(
+                      po + (h / (kGroup / 32) * kTile + 8 * n) * 4);
 #pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            w[0][m] = wq[p][0][m];
-            w[1][m] = wq[p][1][m];
-            sw[m] = ws[p][m];
-          }
-          if (st + kDepth < st1) fetch(wq[p], ws[p], st + kDepth);
-          float sx[kNt][2];
-          if (kX8) {
+                  for (int m = 0; m < 2; ++m) {
+                    part[m][n][0] = o.x;
+                    part[m][n][1] = o.y;
+                    part[m][n][2] = 16.f * o.x;
+                    part[m][n][3] = 16.f * o.y;
+                  }
+                }
+              }
 #pragma unroll
-            for (int n = 0; n < kNt; ++n)
+              for (int j = 0; j < 2; ++j) {
 #pragma unroll
-              for (int i = 0; i < 2; ++i)
-                sx[n][i] = xs_at[n][i] < 0 ? 0.f
-                                           : __ldg(a.x_scale + (int64_t)xs_at[n][i] * a.xs_ld +
-                                                   st * a.xs_step);
-          }
-          float part[2][kNt][4];
+                for (int m = 0; m < 2; ++m) {
+                  const uint32_t word = (h & 1) ? (j ? w[m].w : w[m].z) : (j ? w[m].y : w[m].x);
+                  uint32_t fa[4];
+                  widen(word, fa);
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const int col = 128 * st + 32 * h + 8 * t;
-            uint32_t b[kNt][4];
-#pragma unroll
-            for (int n = 0; n < kNt; ++n)
-              if (n < n_act) load_x<kX8>(a.x, x_at[n] + col, x_at[n] >= 0 && col < a.cols, b[n]);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
+                  for (int n = 0; n < kN; ++n)
+                    mma<kX8>(part[m][n], fa, j ? b[n].z : b[n].x, j ? b[n].w : b[n].y);
+                }
+              }
+              if ((h + 1) % (kGroup / 32) != 0) continue;
+              const int gi = kGroup == 128 ? h / 4 : min(h / (kGroup / 32), g_last);
 #pragma unroll
               for (int m = 0; m < 2; ++m) {
-                const uint4& v = w[h >> 1][m];
-                const uint32_t word = (h & 1) ? (j ? v.w : v.z) : (j ? v.y : v.x);
-                uint32_t fa[4];
-                widen<kX8>(word, fa);
+                const uint32_t sw = ps[(m * kSteps + gi) * 8];
+                const float lo = __uint_as_float(sw << 16), up = __uint_as_float(sw & 0xffff0000u);
 #pragma unroll
-                for (int n = 0; n < kNt; ++n)
-                  if (n < n_act)
-                    mma<kX8>(part[m][n], fa, b[n][2 * j], b[n][2 * j + 1],
-                             j == 0 && h % (kGroup / 32) == 0);
-              }
-            }
-            if ((h + 1) % (kGroup / 32) != 0) continue;
-            const int gi = h / (kGroup / 32);
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              const uint32_t s =
-                  kSteps == 1 ? sw[m] : __shfl_sync(0xffffffffu, sw[m], gi * 8 + g);
-              const float lo = __uint_as_float(s << 16), up = __uint_as_float(s & 0xffff0000u);
-#pragma unroll
-              for (int n = 0; n < kNt; ++n) {
-                if (n >= n_act) continue;
-                if (kX8) {
-                  acc[m][n][0] = fmaf(part[m][n][0], lo * sx[n][0], acc[m][n][0]);
-                  acc[m][n][1] = fmaf(part[m][n][1], lo * sx[n][1], acc[m][n][1]);
-                  acc[m][n][2] = fmaf(part[m][n][2], up * sx[n][0], acc[m][n][2]);
-                  acc[m][n][3] = fmaf(part[m][n][3], up * sx[n][1], acc[m][n][3]);
-                } else {
-                  acc[m][n][0] = fmaf(part[m][n][0], lo, acc[m][n][0]);
-                  acc[m][n][1] = fmaf(part[m][n][1], lo, acc[m][n][1]);
-                  acc[m][n][2] = fmaf(part[m][n][2], up, acc[m][n][2]);
-                  acc[m][n][3] = fmaf(part[m][n][3], up, acc[m][n][3]);
+                for (int n = 0; n < kN; ++n) {
+                  if (kX8) {
+                    const float2 xs = *reinterpret_cast<const float2*>(pxs + (h / 4 * kTile + 8 * n) * 4);
+                    acc[m][n][0] = fmaf(part[m][n][0], lo * xs.x, acc[m][n][0]);
+                    acc[m][n][1] = fmaf(part[m][n][1], lo * xs.y, acc[m][n][1]);
+                    acc[m][n][2] = fmaf(part[m][n][2], up * xs.x, acc[m][n][2]);
+                    acc[m][n][3] = fmaf(part[m][n][3], up * xs.y, acc[m][n][3]);
+                  } else {
+                    acc[m][n][0] = fmaf(part[m][n][0], lo, acc[m][n][0]);
+                    acc[m][n][1] = fmaf(part[m][n][1], lo, acc[m][n][1]);
+                    acc[m][n][2] = fmaf(part[m][n][2], up, acc[m][n][2]);
+                    acc[m][n][3] = fmaf(part[m][n][3], up, acc[m][n][3]);
+                  }
                 }
               }
             }
           }
+          px += 512 << im.log2;
+          po += kSteps * kTile * 4 << im.log2;
+          if (kX8) pxs += 2 * kTile * 4 << im.log2;
+          __syncwarp();  // the slot's scales have been read
+          fetch(at);
+          at = at + kStep == kDepth * kStep ? 0 : at + kStep;
+        }
+          if (copied) break;
+          copied = true;
+          if (end - c0 < kDepth) {
+            copies_wait<0>();
+            make_chunk();
+          }
+          copy_chunk();
+        }
+        if (end - c0 >= kDepth) make_chunk();  // the next chunk landed a chunk ago
+        if (lane == 0) tc::mbar_arrive(&s_free[buf]);
+        if (++buf == kBuffers) {
+          buf = 0;
+          x_phase ^= 1;
         }
       }
+    };
+    const int n_act = (im.tile_rows + 7) / 8;
+    if constexpr (kNt == 1) {
+      steps(std::integral_constant<int, 1>{});
+    } else {
+      if (n_act == 1)
+        steps(std::integral_constant<int, 1>{});
+      else
+        steps(std::integral_constant<int, 2>{});
     }
-    if (split > 1) {
-      __syncthreads();  // the previous item's sums have been read
-      float* mine = s_red + (size_t)warp * (8 * kNt * 32) + lane;
+    if (im.split > 1) {
+      __syncthreads();  // the last unit's sums have been read
+      // the warps but the first of each pair leave theirs
+      const int place = (warp >> im.log2) * (im.split - 1) + ks - 1;
+      float* sums = reinterpret_cast<float*>(s_x + kBuffers * a.buf_bytes) +
+                    place * (8 * kNt * 32) + lane;
+      if (ks != 0) {
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int n = 0; n < kNt; ++n)
+          for (int n = 0; n < kNt; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mine[((m * kNt + n) * 4 + i) * 32] = acc[m][n][i];
+            for (int i = 0; i < 4; ++i) sums[((m * kNt + n) * 4 + i) * 32] = acc[m][n][i];
+      }
       __syncthreads();
       if (ks == 0) {
-        for (int w = 1; w < split; ++w) {
-          const float* other = mine + (size_t)w * (8 * kNt * 32);
+        for (int o = 1; o < im.split; ++o) {
+          const float* other = sums + o * (8 * kNt * 32);
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -389,31 +673,69 @@ __global__ void __launch_bounds__(kThreads, kNt == 4 ? 1 : 2) w4_kernel(const Ar
         }
       }
     }
-    if (!valid || ks != 0) continue;
+    if constexpr (kCluster) {
+      // the first block of the cluster adds the others' sums, in order, some pairs at a time
+      cg::cluster_group cluster = cg::this_cluster();
+      const int mine = warp >> im.log2;
+      float* sums = reinterpret_cast<float*>(s_x + kBuffers * a.buf_bytes) +
+                    mine % kHandOver * (8 * kNt * 32) + lane;
+      if (im.split > 1) __syncthreads();  // the block's own sums have been read
+      for (int first = 0; first < kWarps >> im.log2; first += kHandOver) {
+        const bool now = ks == 0 && mine / kHandOver * kHandOver == first;
+        if (now && rank != 0) {
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < kNt; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) sums[((m * kNt + n) * 4 + i) * 32] = acc[m][n][i];
+        }
+        cluster.sync();
+        if (now && rank == 0) {
+          for (int o = 1; o < per; ++o) {
+            const float* other = cluster.map_shared_rank(sums, o);
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int n = 0; n < kNt; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[m][n][i] += other[((m * kNt + n) * 4 + i) * 32];
+          }
+        }
+        cluster.sync();
+      }
+      if (rank != 0) continue;
+    }
+    if (dead || n_mine == 0 || ks != 0) continue;
 #pragma unroll
     for (int n = 0; n < kNt; ++n) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 8 * n + 2 * t + (i & 1);
-        if (r >= tile_rows) continue;
-        const int64_t o = (out_row0 + r) * a.rows;
+      for (int j = 0; j < 2; ++j) {
+        const int r = 8 * n + 2 * t + j;
+        if (r >= im.tile_rows) continue;
+        // a row index out of range is reported, and its row reads as zeros
+        const bool known = row_of(im, r) >= 0;
+        if (!known) report_status(a.status, kStatusInvalidInput);
+        const int64_t o = (im.out_row0 + r) * a.rows;
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          float v = acc[m][n][i];
-          int b = pair;
+        for (int q = 0; q < 4; ++q) {
+          const int m = q >> 1, i = (q & 1) * 2 + j;  // block, and row g or g + 8 of it
+          if (a.parts == 2 && m == 1) continue;
+          const float u = code_unit<kX8>(q & 1);
+          float v = acc[m][n][i] * u;
+          const int b = a.parts == 2 ? pair : 2 * pair + m;
           if (a.parts == 2) {
-            if (m == 1) continue;
-            float up = acc[1][n][i];
+            float up = acc[1][n][i] * u;
             if (a.clamp > 0.f) {
               v = clip(v, a.clamp);
               up = clip(up, a.clamp);
             }
             v = v / (1.f + expf(-v)) * up;
-          } else {
-            b = 2 * pair + m;
-            if (a.act == 2) v = v < 0.f ? 0.f : v;
+          } else if (a.relu) {
+            v = v < 0.f ? 0.f : v;
           }
-          const int row = 16 * b + g + 8 * (i >> 1);
+          if (!known) v = 0.f;
+          const int row = 16 * b + g + 8 * (q & 1);
           if (row >= a.rows) continue;
           if (a.out_f32)
             static_cast<float*>(a.out)[o + row] = v;
@@ -423,13 +745,52 @@ __global__ void __launch_bounds__(kThreads, kNt == 4 ? 1 : 2) w4_kernel(const Ar
       }
     }
   }
+  copies_wait<0>();  // nothing is in flight when the block ends
 }
 
-template <int kNt, bool kX8>
+template <int kNt, bool kX8, int kGroup, bool kCluster>
+cudaError_t launch_one(const Args& a, int grid, size_t smem, cudaStream_t stream) {
+  const auto kernel = w4_kernel<kNt, kX8, kGroup, kCluster>;
+  static std::atomic<bool> ready[64];  // the attribute is set once on each device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !ready[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynamicSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready[dev].store(true, std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = 32 * kWarps;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kCluster ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <int kNt, bool kX8, bool kCluster>
 cudaError_t launch_group(const Args& a, int group, int grid, size_t smem, cudaStream_t stream) {
-  if (group == 32) return launch_pdl(w4_kernel<kNt, kX8, 32>, grid, kThreads, smem, stream, a);
-  if (group == 64) return launch_pdl(w4_kernel<kNt, kX8, 64>, grid, kThreads, smem, stream, a);
-  return launch_pdl(w4_kernel<kNt, kX8, 128>, grid, kThreads, smem, stream, a);
+  return group == 32   ? launch_one<kNt, kX8, 32, kCluster>(a, grid, smem, stream)
+         : group == 64 ? launch_one<kNt, kX8, 64, kCluster>(a, grid, smem, stream)
+                       : launch_one<kNt, kX8, 128, kCluster>(a, grid, smem, stream);
+}
+
+template <bool kX8>
+cudaError_t launch_tile(const Args& a, int nt, int group, int grid, size_t smem,
+                        cudaStream_t stream) {
+  if (nt == 1)
+    return a.cluster > 1 ? launch_group<1, kX8, true>(a, group, grid, smem, stream)
+                         : launch_group<1, kX8, false>(a, group, grid, smem, stream);
+  return a.cluster > 1 ? launch_group<2, kX8, true>(a, group, grid, smem, stream)
+                       : launch_group<2, kX8, false>(a, group, grid, smem, stream);
 }
 
 // One block turns 16 rows x 128 columns of bf16 weights into codes and scales.  A group's scale
@@ -514,11 +875,12 @@ cudaError_t launch_w4(const W4Gemm& p, cudaStream_t stream, int* launches) {
   a.n_groups = p.n_groups;
   a.has_shared = p.has_shared;
   a.max_rows = p.max_rows;
+  a.max_group_rows = p.max_group_rows;
   a.shared_rows = p.shared_rows;
   a.shared_x_row0 = p.shared_x_row0;
   a.shared_out_row0 = p.shared_out_row0;
-  a.items_per_tile = p.parts == 2 ? a.rb : (a.rb + 1) / 2;
-  a.act = p.relu ? 2 : 0;
+  a.pairs = p.parts == 2 ? a.rb : (a.rb + 1) / 2;
+  a.relu = p.relu;
   a.clamp = p.clamp;
   a.out = p.out;
   a.out_f32 = p.out_f32;
@@ -526,30 +888,56 @@ cudaError_t launch_w4(const W4Gemm& p, cudaStream_t stream, int* launches) {
   // rows of a tile: enough for the largest group there can be, 32 at most
   const int64_t most = p.has_shared ? (p.shared_rows > p.max_group_rows ? p.shared_rows : p.max_group_rows)
                                     : p.max_group_rows;
-  const int nt = most <= 8 ? 1 : most <= 16 ? 2 : 4;
-  // split the columns among warps until there are about 16 warps' loads in flight on each SM,
-  // four steps or more to a warp
+  const int nt = most <= 8 ? 1 : 2;
+  const bool x8 = p.x_scale != nullptr;
   const int sms = tc::num_sms();
-  const int64_t groups = (p.max_rows < p.n_groups ? p.max_rows : p.n_groups) + p.has_shared;
-  const int64_t items = groups * a.items_per_tile;
-  a.split = 1;
-  while (a.split < kWarps && items * a.split < 16 * sms && (a.ku + 1) / 2 >= 8 * a.split)
-    a.split *= 2;
-  const int64_t tile = 8 * nt;
-  const int64_t tiles = p.max_rows / tile + (p.max_rows < p.n_groups ? p.max_rows : p.n_groups) +
-                        (p.has_shared ? (p.shared_rows + tile - 1) / tile : 0);
-  const int64_t blocks = (tiles * a.items_per_tile * a.split + kWarps - 1) / kWarps;
-  const int64_t full = (nt == 4 ? 1 : 2) * (int64_t)sms;
-  const int grid = (int)(blocks < 1 ? 1 : blocks < full ? blocks : full);
-  const size_t smem = a.split > 1 ? sizeof(float) * kWarps * 8 * nt * 32 : 0;
+  const int tile = 8 * nt, n_steps = (a.ku + 3) / 4;
+  const int rows = (int)(most < tile ? most : tile);  // the most of a tile
+  // shared memory: the rings, the partial sums, and three buffers of input rows, in which a
+  // chunk of a step for each share of a cut item has to fit
+  const auto buffer = [&](int split, int cluster) {
+    const int room = (kDynamicSmem - kWarps * kDepth * kStep -
+                      sum_bytes(nt, split, cluster)) / kBuffers / 16 * 16;
+    const int all = x_bytes(x8, tile, rows, n_steps < 16 ? n_steps : 16, p.group);
+    return room < all ? room : all;
+  };
+  const auto max_split = [&](int cluster) {
+    int split = 1;
+    while (split < kWarps && 2 * split * cluster <= n_steps &&
+           x_steps_of(buffer(2 * split, cluster), x8, tile, rows, p.group) >= 2 * split)
+      split *= 2;
+    return split;
+  };
+  // Clusters of 1, 2, 4 or 8 blocks (of 8, two to each of the device's eight clusters of SMs),
+  // whichever has the items that are expected done first; a unit's hand-over takes about a step.
+  const int64_t shared_tiles = p.has_shared ? (p.shared_rows + tile - 1) / tile : 0;
+  const int64_t reached = p.max_rows < p.n_groups ? p.max_rows : p.n_groups;
+  const int64_t chunks = (a.pairs + kWarps - 1) / kWarps;
+  const int64_t expected = ((p.offsets == nullptr ? (p.max_rows + tile - 1) / tile : reached) +
+                            shared_tiles) * chunks;
+  const auto clusters_of = [&](int c) { return c == 8 && sms >= 144 ? 16 : sms / c; };
+  int64_t least = -1;
+  for (int c = 1; c <= 8 && c <= n_steps && c <= sms; c *= 2) {
+    const int n = clusters_of(c), steps = (n_steps + c - 1) / c;
+    int64_t rest = cost_of(expected % n, n, steps, 0);
+    for (int k = 1; 1 << k <= max_split(c); ++k)
+      rest = std::min(rest, cost_of(expected % n, n, steps, k));
+    const int64_t cost = expected / n * (2 * steps + 1) + rest +
+                         (c > 1 ? (expected + n - 1) / n * 2 : 0);
+    if (least < 0 || cost < least) least = cost, a.cluster = c;
+  }
+  a.max_split = max_split(a.cluster);
+  a.buf_bytes = buffer(a.max_split, a.cluster);
+  const int64_t tiles = p.max_rows / tile + reached + shared_tiles;
+  const int64_t units = tiles * chunks * a.max_split;
+  if (units > INT32_MAX) return cudaErrorInvalidValue;
+  const int64_t n = clusters_of(a.cluster);
+  const int grid = (int)(units < 1 ? 1 : units < n ? units : n) * a.cluster;
+  const size_t bytes = (size_t)kWarps * kDepth * kStep +
+                       sum_bytes(nt, a.max_split, a.cluster) + kBuffers * (size_t)a.buf_bytes;
   ++*launches;
-  if (p.x_scale != nullptr)
-    return nt == 1   ? launch_group<1, true>(a, p.group, grid, smem, stream)
-           : nt == 2 ? launch_group<2, true>(a, p.group, grid, smem, stream)
-                     : launch_group<4, true>(a, p.group, grid, smem, stream);
-  return nt == 1   ? launch_group<1, false>(a, p.group, grid, smem, stream)
-         : nt == 2 ? launch_group<2, false>(a, p.group, grid, smem, stream)
-                   : launch_group<4, false>(a, p.group, grid, smem, stream);
+  return x8 ? launch_tile<true>(a, nt, p.group, grid, bytes, stream)
+            : launch_tile<false>(a, nt, p.group, grid, bytes, stream);
 }
 
 }  // namespace moe
