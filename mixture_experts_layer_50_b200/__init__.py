@@ -30,7 +30,9 @@ _NATIVE_NAMES = {
 
 def __getattr__(name):
     if name in _NATIVE_NAMES:
-        return getattr(importlib.import_module("._native", __name__), name)
+        value = getattr(importlib.import_module("._native", __name__), name)
+        globals()[name] = value  # looked up once
+        return value
     if name == "MoELayer":
         return importlib.import_module(".layer", __name__).MoELayer
     if name == "EPMoELayer":

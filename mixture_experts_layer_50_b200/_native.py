@@ -184,7 +184,9 @@ def _host_ptr(t) -> int:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # (what torch.cuda.current_stream().cuda_stream gives, without the object)
+        torch.cuda.init()
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -334,6 +336,10 @@ def _typed(t, name, dtype, *shape):
     """Pointer of an optional tensor of the current device whose type and shape are checked."""
     if t is None:
         return None
+    if t.shape == shape and (t.dtype is dtype or (type(dtype) is tuple and t.dtype in dtype)) \
+            and t.is_cuda and t.get_device() == torch._C._cuda_getDevice() \
+            and t.is_contiguous():
+        return t.data_ptr()
     p = _ptr(t)
     if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
         raise ValueError(f"{name} has dtype {t.dtype}, not {dtype}")

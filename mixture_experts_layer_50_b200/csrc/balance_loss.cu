@@ -10,12 +10,13 @@
 // As sum_j p_tj = 1, any constant may be taken off f: the kernel uses f_i - 1/E, so that a
 // nearly balanced batch loses no digits in the difference.
 //
-// Two launches.  A cluster of kCountCtas blocks counts the assignments (integers; the blocks'
-// counts meet over distributed shared memory) and clears the accumulators of the second launch,
-// so nothing has to be zero before the call.  Then every token's row is read once: its
-// probabilities give its gradient row, and add to P.  P is added up in 64-bit fixed point,
-// which makes its value independent of the order of the atomic additions; the last block to
-// finish turns the sums into P and the loss.
+// Two launches.  Clusters of kCountCtas blocks, one for every kCountIds assignments, count them
+// (integers; a cluster's counts meet over distributed shared memory and are written once) and
+// clear the accumulators of the second launch, so nothing has to be zero before the call.  Then
+// every token's row is read once: its probabilities give its gradient row, and add to P.  P is
+// added up in 64-bit fixed point, which makes its value independent of the order of the atomic
+// additions; the last block to finish turns the sums into P and the loss.  (Additions to shared
+// memory bound the count: one cluster took 15 us for 16384 tokens of six experts.)
 //
 // Bound: one read of the logits and one write of the gradient.
 #include <cooperative_groups.h>
@@ -29,24 +30,27 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kCountCtas = 8;
-constexpr int kCountThreads = 512;
+constexpr int kCountThreads = 1024;
+constexpr int kCountUnroll = 4;
+constexpr int kCountIds = 8192, kMaxCounts = 16;
 constexpr int kLossThreads = 256;
 
-// Scratch of one call (device): sums [E] u64, f0 [E], f [E], then T and the ticket.
+// Scratch of one call (device): sums [E] u64, the clusters' counts [n][E] and tokens [n], and
+// the ticket.
 struct LossScratch {
   unsigned long long* sums;
-  float* f0;
-  float* f;
-  int32_t* n_tokens;
+  int32_t* counts;
+  int32_t* tokens;
   unsigned* ticket;
+  int n;  // clusters
 };
-LossScratch scratch_of(void* p, int E) {
+LossScratch scratch_of(void* p, int E, int n) {
   LossScratch s;
   s.sums = static_cast<unsigned long long*>(p);
-  s.f0 = reinterpret_cast<float*>(s.sums + E);
-  s.f = s.f0 + E;
-  s.n_tokens = reinterpret_cast<int32_t*>(s.f + E);
-  s.ticket = reinterpret_cast<unsigned*>(s.n_tokens + 1);
+  s.counts = reinterpret_cast<int32_t*>(s.sums + E);
+  s.tokens = s.counts + (size_t)kMaxCounts * E;
+  s.ticket = reinterpret_cast<unsigned*>(s.tokens + kMaxCounts);
+  s.n = n;
   return s;
 }
 
@@ -62,42 +66,54 @@ __global__ void __cluster_dims__(kCountCtas, 1, 1) __launch_bounds__(kCountThrea
   __syncthreads();
   bool bad = false;
   // N * k is below 2^30 (checked on the host), so are all indices
-  const uint32_t stride = kCountCtas * kCountThreads, nk = (uint32_t)(N * k);
-  for (uint32_t i = rank * kCountThreads + threadIdx.x; i < nk; i += stride) {
-    if (mask != nullptr && mask[i / (uint32_t)k] == 0) continue;
-    const int e = ids[i];
-    if (e >= 0 && e < E)
-      atomicAdd(&s_count[e], 1);
-    else
-      bad = true;
+  const uint32_t stride = gridDim.x * kCountThreads, nk = (uint32_t)(N * k);
+  const uint32_t first = blockIdx.x * kCountThreads + threadIdx.x;
+  for (uint32_t i = first; i < nk; i += kCountUnroll * stride) {
+    // all loads of a turn are in flight before its first addition
+    int e[kCountUnroll];
+    bool on[kCountUnroll];
+#pragma unroll
+    for (int j = 0; j < kCountUnroll; ++j) {
+      const uint32_t at = i + j * stride;
+      on[j] = at < nk;
+      e[j] = on[j] ? ids[at] : 0;
+    }
+    if (mask != nullptr) {
+#pragma unroll
+      for (int j = 0; j < kCountUnroll; ++j)
+        if (on[j]) on[j] = mask[(i + j * stride) / (uint32_t)k] != 0;
+    }
+#pragma unroll
+    for (int j = 0; j < kCountUnroll; ++j) {
+      if (!on[j]) continue;
+      if (e[j] >= 0 && e[j] < E)
+        atomicAdd(&s_count[e[j]], 1);
+      else
+        bad = true;
+    }
   }
   if (mask != nullptr) {
     int n = 0;
-    for (uint32_t t = rank * kCountThreads + threadIdx.x; t < (uint32_t)N; t += stride)
+    for (uint32_t t = first; t < (uint32_t)N; t += stride)
       n += mask[t] != 0;
     for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
     if ((threadIdx.x & 31) == 0 && n != 0) atomicAdd(&s_count[E], n);
   }
   if (bad) report_status(status, kStatusInvalidInput);
   cluster.sync();
-  int64_t tokens = N;
-  if (mask != nullptr) {
-    tokens = 0;
-    for (int b = 0; b < kCountCtas; ++b) tokens += cluster.map_shared_rank(s_count, b)[E];
+  const int c = (int)blockIdx.x / kCountCtas;
+  for (int e = rank * kCountThreads + threadIdx.x; e <= E; e += kCountCtas * kCountThreads) {
+    int n = 0;
+    for (int b = 0; b < kCountCtas; ++b) n += cluster.map_shared_rank(s_count, b)[e];
+    if (e == E) {
+      out.tokens[c] = mask != nullptr ? n : c == 0 ? (int32_t)N : 0;
+      continue;
+    }
+    out.counts[c * E + e] = n;
+    if (counts != nullptr) counts[e] = n;  // (given where there is one cluster)
+    if (c == 0) out.sums[e] = 0;
   }
-  const double per = 1.0 / ((double)(tokens > 0 ? tokens : 1) * k);
-  for (int e = rank * kCountThreads + threadIdx.x; e < E; e += kCountCtas * kCountThreads) {
-    int c = 0;
-    for (int b = 0; b < kCountCtas; ++b) c += cluster.map_shared_rank(s_count, b)[e];
-    if (counts != nullptr) counts[e] = c;
-    out.f[e] = (float)(c * per);
-    out.f0[e] = (float)(c * per - 1.0 / E);
-    out.sums[e] = 0;
-  }
-  if (rank == 0 && threadIdx.x == 0) {
-    *out.n_tokens = (int32_t)tokens;
-    *out.ticket = 0;
-  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *out.ticket = 0;
   cluster.sync();  // no block leaves while another reads its counts
 }
 
@@ -109,10 +125,12 @@ struct LossArgs {
   float alpha;
   const float* grad_loss;  // the gradient of the loss (device), or null: 1
   float* loss;
+  int32_t* counts;  // where the count kernel has not written them
   float* P;
   float* dlogits;
   int accumulate;
   int want_sums;
+  int k;
   float fixed_scale;  // power of two; N * fixed_scale < 2^62
   LossScratch s;
 };
@@ -130,35 +148,73 @@ __device__ __forceinline__ float team_max(float v) {
   return v;
 }
 
-// kTeam lanes own a token; lane i of the team holds experts i, i + kTeam, ...: kEpl of them.
-template <int kTeam, int kEpl, bool kSigmoid>
+// kTeam lanes own a token.  Lane i of the team holds kEpl experts: i, i + kTeam, ..., or with
+// kVec, in runs of four, 4 i ... 4 i + 3, 4 (i + kTeam) ....
+template <int kTeam, bool kVec>
+__device__ __forceinline__ int expert_of(int ti, int j) {
+  return kVec ? 4 * (ti + j / 4 * kTeam) + j % 4 : ti + j * kTeam;
+}
+
+template <int kTeam, int kEpl, bool kVec, bool kSigmoid>
 __global__ void __launch_bounds__(kLossThreads) balance_loss_kernel(const LossArgs a) {
   constexpr int kTeams = kLossThreads / kTeam;
   pdl_wait();
-  extern __shared__ float s_p[];  // [kTeams][E]
+  extern __shared__ float s_f[];  // f [E]; then [kTeams][E] sums
   const int E = a.E;
+  float* const s_p = s_f + E;
   const int ti = threadIdx.x % kTeam, team = threadIdx.x / kTeam;
-  const int T = *a.s.n_tokens;
+  int T = 0;
+  for (int c = 0; c < a.s.n; ++c) T += a.s.tokens[c];
+  const double per = 1.0 / ((double)(T > 0 ? T : 1) * a.k);
+  for (int e = threadIdx.x; e < E; e += kLossThreads) {
+    int n = 0;
+#pragma unroll 4
+    for (int c = 0; c < a.s.n; ++c) n += a.s.counts[c * E + e];
+    s_f[e] = (float)(n * per);
+    s_p[e] = (float)(n * per - 1.0 / E);
+    if (a.counts != nullptr && blockIdx.x == 0) a.counts[e] = n;
+  }
+  __syncthreads();
   const float g = (a.grad_loss != nullptr ? *a.grad_loss : 1.f) * a.alpha * (float)E /
                   (float)(T > 0 ? T : 1);
   float f0[kEpl], acc[kEpl];
 #pragma unroll
   for (int j = 0; j < kEpl; ++j) {
-    const int e = ti + j * kTeam;
-    f0[j] = e < E ? a.s.f0[e] : 0.f;
+    const int e = expert_of<kTeam, kVec>(ti, j);
+    f0[j] = e < E ? s_p[e] : 0.f;
     acc[j] = 0.f;
   }
-  // every team of the block takes the same number of steps: the shuffles need whole warps
-  for (int64_t t0 = (int64_t)blockIdx.x * kTeams; t0 < a.N; t0 += (int64_t)gridDim.x * kTeams) {
-    const int64_t t = t0 + team;
+  // a token's logits, -infinity where there are none
+  auto load = [&](int64_t t, float (&z)[kEpl]) {
     const bool live = t < a.N && (a.mask == nullptr || a.mask[t] != 0);
-    const float* z = a.logits + t * E;
+#pragma unroll
+    for (int j = 0; j < kEpl; j += kVec ? 4 : 1) {
+      const int e = expert_of<kTeam, kVec>(ti, j);
+      const bool in = live && e < E;
+      if constexpr (kVec) {
+        const float4 v = in ? __ldg(reinterpret_cast<const float4*>(a.logits + t * E + e))
+                            : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        z[j] = v.x;
+        z[j + 1] = v.y;
+        z[j + 2] = v.z;
+        z[j + 3] = v.w;
+      } else {
+        z[j] = in ? __ldg(a.logits + t * E + e) : -INFINITY;
+      }
+    }
+    return live;
+  };
+  // every team of the block takes the same number of steps: the shuffles need whole warps
+  const int64_t step = (int64_t)gridDim.x * kTeams;
+  float next[kEpl];
+  bool next_live = load((int64_t)blockIdx.x * kTeams + team, next);
+  for (int64_t t0 = (int64_t)blockIdx.x * kTeams; t0 < a.N; t0 += step) {
+    const int64_t t = t0 + team;
+    const bool live = next_live;
     float p[kEpl], u[kEpl];
 #pragma unroll
-    for (int j = 0; j < kEpl; ++j) {
-      const int e = ti + j * kTeam;
-      p[j] = live && e < E ? z[e] : -INFINITY;
-    }
+    for (int j = 0; j < kEpl; ++j) p[j] = next[j];
+    if (t0 + step < a.N) next_live = load(t + step, next);
     float sum = 0.f;
     if (kSigmoid) {
 #pragma unroll
@@ -192,26 +248,40 @@ __global__ void __launch_bounds__(kLossThreads) balance_loss_kernel(const LossAr
       acc[j] += p[j];
       dot = fmaf(p[j], f0[j], dot);
     }
+    if (a.dlogits == nullptr) continue;
     dot = team_sum<kTeam>(dot);
-    if (a.dlogits != nullptr && t < a.N) {
-      float* dz = a.dlogits + t * E;
+    if (t >= a.N) continue;
 #pragma unroll
-      for (int j = 0; j < kEpl; ++j) {
-        const int e = ti + j * kTeam;
-        if (e >= E) continue;
-        float v = live ? g * (p[j] * (f0[j] - dot)) : 0.f;
-        if (kSigmoid && live) v *= u[j];
-        if (!a.accumulate)
-          dz[e] = v;
-        else if (live)
-          dz[e] += v;
+    for (int j = 0; j < kEpl; ++j) {
+      p[j] = live ? g * (p[j] * (f0[j] - dot)) : 0.f;
+      if (kSigmoid && live) p[j] *= u[j];
+    }
+    if (a.accumulate && !live) continue;
+#pragma unroll
+    for (int j = 0; j < kEpl; j += kVec ? 4 : 1) {
+      const int e = expert_of<kTeam, kVec>(ti, j);
+      if (e >= E) continue;
+      float* dz = a.dlogits + t * E + e;
+      if constexpr (kVec) {
+        float4 v = make_float4(p[j], p[j + 1], p[j + 2], p[j + 3]);
+        if (a.accumulate) {
+          const float4 o = *reinterpret_cast<const float4*>(dz);
+          v.x += o.x;
+          v.y += o.y;
+          v.z += o.z;
+          v.w += o.w;
+        }
+        *reinterpret_cast<float4*>(dz) = v;
+      } else {
+        *dz = a.accumulate ? *dz + p[j] : p[j];
       }
     }
   }
   if (!a.want_sums) return;
+  __syncthreads();  // f - 1/E has been read
 #pragma unroll
   for (int j = 0; j < kEpl; ++j) {
-    const int e = ti + j * kTeam;
+    const int e = expert_of<kTeam, kVec>(ti, j);
     if (e < E) s_p[team * E + e] = acc[j];
   }
   __syncthreads();
@@ -225,19 +295,21 @@ __global__ void __launch_bounds__(kLossThreads) balance_loss_kernel(const LossAr
       atomicAdd(&a.s.sums[e], (unsigned long long)((double)v * (double)a.fixed_scale));
   }
   __shared__ bool s_last;
-  __threadfence();
   __syncthreads();
-  if (threadIdx.x == 0) s_last = atomicAdd(a.s.ticket, 1u) == gridDim.x - 1;
+  if (threadIdx.x == 0) {
+    __threadfence();  // the block's additions come before its ticket
+    s_last = atomicAdd(a.s.ticket, 1u) == gridDim.x - 1;
+    __threadfence();
+  }
   __syncthreads();
   if (!s_last) return;
-  __threadfence();
   double part = 0.0;
   for (int e = threadIdx.x; e < E; e += kLossThreads) {
     const unsigned long long v = __ldcg(&a.s.sums[e]);
     const double Pe = (v >> 63) ? (double)NAN
                                 : (double)v / ((double)a.fixed_scale * (T > 0 ? T : 1));
     if (a.P != nullptr) a.P[e] = (float)Pe;
-    part += (double)a.s.f[e] * Pe;
+    part += (double)s_f[e] * Pe;
   }
   __shared__ double s_sum[kLossThreads];
   s_sum[threadIdx.x] = part;
@@ -249,50 +321,66 @@ __global__ void __launch_bounds__(kLossThreads) balance_loss_kernel(const LossAr
     a.loss[0] = (float)((double)a.alpha * E * s_sum[0]);
 }
 
-template <int kTeam, int kEpl>
+template <int kTeam, int kEpl, bool kVec>
 cudaError_t launch_rows(const LossArgs& a, bool sigmoid, int sms, cudaStream_t stream) {
   constexpr int kTeams = kLossThreads / kTeam;
-  const size_t smem = a.want_sums ? sizeof(float) * kTeams * a.E : 0;
+  const size_t smem = sizeof(float) * a.E * (1 + (a.want_sums ? kTeams : 1));
   const int64_t want = (a.N + kTeams - 1) / kTeams;
-  const int grid = (int)(want < 1 ? 1 : want < 4 * sms ? want : 4 * sms);
-  return sigmoid ? launch_pdl(balance_loss_kernel<kTeam, kEpl, true>, grid, kLossThreads, smem,
-                              stream, a)
-                 : launch_pdl(balance_loss_kernel<kTeam, kEpl, false>, grid, kLossThreads, smem,
-                              stream, a);
+  // blocks that the registers let be on an SM at once
+  const int per_sm = kEpl <= 2 ? 6 : kEpl == 4 ? 5 : kEpl == 8 ? (sigmoid ? 3 : 4)
+                   : kEpl == 12 ? (sigmoid ? 2 : 3) : kEpl == 16 ? 2 : 1;
+  const int grid = (int)(want < 1 ? 1 : want < per_sm * sms ? want : per_sm * sms);
+  return sigmoid ? launch_pdl(balance_loss_kernel<kTeam, kEpl, kVec, true>, grid, kLossThreads,
+                              smem, stream, a)
+                 : launch_pdl(balance_loss_kernel<kTeam, kEpl, kVec, false>, grid, kLossThreads,
+                              smem, stream, a);
+}
+
+// More than 64 experts: 16 bytes at a time where rows start on 16 bytes.
+template <int kEpl>
+cudaError_t launch_wide(const LossArgs& a, bool sigmoid, int sms, cudaStream_t stream) {
+  const auto off = reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.dlogits);
+  return a.E % 4 == 0 && off % 16 == 0 ? launch_rows<32, kEpl, true>(a, sigmoid, sms, stream)
+                                       : launch_rows<32, kEpl, false>(a, sigmoid, sms, stream);
 }
 
 }  // namespace
 
-size_t balance_loss_scratch_bytes(int E) { return (size_t)E * 16 + 8; }
+size_t balance_loss_scratch_bytes(int E) {
+  return (size_t)E * (8 + 4 * kMaxCounts) + 4 * kMaxCounts + 8;
+}
 
 cudaError_t launch_balance_loss(const float* logits, const int32_t* ids, const uint8_t* mask,
                                 int64_t N, int E, int k, int score_fn, float alpha,
                                 const float* grad_loss, float* loss, int32_t* counts, float* P,
                                 float* dlogits, int accumulate, void* scratch, int* status,
                                 cudaStream_t stream, int* launches) {
-  const LossScratch s = scratch_of(scratch, E);
-  cudaError_t e = launch_pdl(balance_count_kernel, kCountCtas, kCountThreads,
-                             sizeof(int32_t) * (E + 1), stream, ids, mask, N, E, k, counts, s,
-                             status);
+  const bool rows = loss != nullptr || P != nullptr || dlogits != nullptr;
+  int64_t n = rows ? (N * k + kCountIds - 1) / kCountIds : 1;
+  n = n < 1 ? 1 : n < kMaxCounts ? n : kMaxCounts;
+  const LossScratch s = scratch_of(scratch, E, (int)n);
+  cudaError_t e = launch_pdl(balance_count_kernel, (unsigned)n * kCountCtas, kCountThreads,
+                             sizeof(int32_t) * (E + 1), stream, ids, mask, N, E, k,
+                             n == 1 ? counts : nullptr, s, status);
   ++*launches;
   if (e != cudaSuccess) return e;
-  if (loss == nullptr && P == nullptr && dlogits == nullptr) return cudaSuccess;
-  LossArgs a{logits, mask, N, E, alpha, grad_loss, loss, P, dlogits, accumulate,
-             loss != nullptr || P != nullptr, 0.f, s};
+  if (!rows) return cudaSuccess;
+  LossArgs a{logits, mask, N, E, alpha, grad_loss, loss, n == 1 ? nullptr : counts, P, dlogits,
+             accumulate, loss != nullptr || P != nullptr, k, 0.f, s};
   a.fixed_scale = 1.f;
   for (int64_t v = N; v < (int64_t)1 << 61; v = (v < 1 ? 1 : v) * 2) a.fixed_scale *= 2.f;
   ++*launches;
   const int sms = tc::num_sms();
   const bool sg = score_fn == 1;
-  if (E <= 8) return launch_rows<8, 1>(a, sg, sms, stream);
-  if (E <= 16) return launch_rows<16, 1>(a, sg, sms, stream);
-  if (E <= 32) return launch_rows<32, 1>(a, sg, sms, stream);
-  if (E <= 64) return launch_rows<32, 2>(a, sg, sms, stream);
-  if (E <= 128) return launch_rows<32, 4>(a, sg, sms, stream);
-  if (E <= 256) return launch_rows<32, 8>(a, sg, sms, stream);
-  if (E <= 384) return launch_rows<32, 12>(a, sg, sms, stream);
-  if (E <= 512) return launch_rows<32, 16>(a, sg, sms, stream);
-  return launch_rows<32, 32>(a, sg, sms, stream);
+  if (E <= 8) return launch_rows<8, 1, false>(a, sg, sms, stream);
+  if (E <= 16) return launch_rows<16, 1, false>(a, sg, sms, stream);
+  if (E <= 32) return launch_rows<32, 1, false>(a, sg, sms, stream);
+  if (E <= 64) return launch_rows<32, 2, false>(a, sg, sms, stream);
+  if (E <= 128) return launch_wide<4>(a, sg, sms, stream);
+  if (E <= 256) return launch_wide<8>(a, sg, sms, stream);
+  if (E <= 384) return launch_wide<12>(a, sg, sms, stream);
+  if (E <= 512) return launch_wide<16>(a, sg, sms, stream);
+  return launch_wide<32>(a, sg, sms, stream);
 }
 
 }  // namespace moe

@@ -232,7 +232,11 @@ cudaError_t launch(const NormArgs& a, cudaStream_t stream) {
   }
   const dim3 grid((unsigned)a.N);
   auto threads = [&](int vpt) { return (nvec + 32 * vpt - 1) / (32 * vpt) * 32; };
-  // at most 4096 vectors (checked by the caller): 1024 threads of up to 64 registers
+  // few rows: a vector a thread, for the shortest way through; else as few threads as hold the
+  // row (at most 4096 vectors, checked by the caller: 1024 threads of up to 64 registers)
+  if (a.N < 512 && nvec <= 1024)
+    return launch_pdl(rms_norm_kernel<T, 1, 0>, grid, threads(1), 0, stream, a);
+  if (nvec <= 512) return launch_pdl(rms_norm_kernel<T, 2, 0>, grid, threads(2), 0, stream, a);
   return launch_pdl(rms_norm_kernel<T, 4, 0>, grid, threads(4), 0, stream, a);
 }
 

@@ -167,20 +167,22 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// d += a b
+// d = a b + c
 template <bool kHalf>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                    uint32_t b1) {
+                                    uint32_t b1, const float (&c)[4]) {
   if constexpr (kHalf)
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        "{%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
+          "f"(c[2]), "f"(c[3]));
   else
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        "{%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
+          "f"(c[2]), "f"(c[3]));
 }
 
 // The four A registers of one word of codes: the codes as subnormal numbers, those of rows g + 8
@@ -564,18 +566,16 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
 #pragma unroll
               for (int n = 0; n < kN; ++n)
                 b[n] = *reinterpret_cast<const uint4*>(px + x_off[n] + 64 * h);
+              float off[kN][4];  // what a group's sums start from
               if (h % (kGroup / 32) == 0) {
 #pragma unroll
                 for (int n = 0; n < kN; ++n) {
                   const float2 o = *reinterpret_cast<const float2*>(
                       po + (h / (kGroup / 32) * kTile + 8 * n) * 4);
-#pragma unroll
-                  for (int m = 0; m < 2; ++m) {
-                    part[m][n][0] = o.x;
-                    part[m][n][1] = o.y;
-                    part[m][n][2] = 16.f * o.x;
-                    part[m][n][3] = 16.f * o.y;
-                  }
+                  off[n][0] = o.x;
+                  off[n][1] = o.y;
+                  off[n][2] = 16.f * o.x;
+                  off[n][3] = 16.f * o.y;
                 }
               }
 #pragma unroll
@@ -587,7 +587,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
                   widen(word, fa);
 #pragma unroll
                   for (int n = 0; n < kN; ++n)
-                    mma<kX8>(part[m][n], fa, j ? b[n].z : b[n].x, j ? b[n].w : b[n].y);
+                    mma<kX8>(part[m][n], fa, j ? b[n].z : b[n].x, j ? b[n].w : b[n].y,
+                             j == 0 && h % (kGroup / 32) == 0 ? off[n] : part[m][n]);
                 }
               }
               if ((h + 1) % (kGroup / 32) != 0) continue;
