@@ -54,7 +54,6 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kMaxGroups = 1025;  // 1024 routed groups and the shared one
 
 struct Args {
   const uint4* q;
@@ -63,12 +62,12 @@ struct Args {
   const void* x;
   const float* x_scale;
   int xs_ld, xs_step;  // floats per row; 1: a scale per 128 columns, 0: one per row
-  int64_t x_rows;
+  int x_rows;
   const int32_t* row_index;
   const int32_t* offsets;
   int n_groups, has_shared;
-  int64_t max_rows, max_group_rows, shared_rows, shared_x_row0, shared_out_row0;
-  int pairs, max_split, buf_bytes, cluster, relu;
+  int max_rows, max_group_rows, shared_rows, shared_x_row0, shared_out_row0;
+  int pairs, max_split, x_steps, buf_bytes, tables, cluster, relu;
   float clamp;
   void* out;
   int out_f32;
@@ -78,7 +77,7 @@ struct Args {
 // Warps of a block, as many as the registers allow (one block on an SM), and the steps of 256
 // columns in a warp's ring, of two blocks' weights and scales each.
 constexpr int kWarps = 16, kThreads = 32 * kWarps, kDepth = 2;
-constexpr int kDynamicSmem = 220 * 1024;  // of 227 KB, less the tables
+constexpr int kDynamicSmem = 226 * 1024;  // of 227 KB, less the barriers and small tables
 constexpr int kStepQ = 4096, kStep = kStepQ + 512;
 constexpr int kBuffers = 3;  // of input rows
 
@@ -87,7 +86,8 @@ constexpr int kBuffers = 3;  // of input rows
 // each row, then (8-bit rows) the scales of each 128 columns and row.
 __host__ __device__ constexpr int x_pitch(int steps) { return 512 * steps + 64; }
 __host__ __device__ constexpr int x_bytes(bool x8, int tile, int rows, int steps, int group) {
-  return (rows * x_pitch(steps) + tile * 4 * steps * (256 / group + (x8 ? 2 : 0)) + 15) / 16 * 16;
+  return (rows * x_pitch(steps) + tile * 4 * steps * (256 / group + (x8 ? 2 : 0)) + 127) /
+         128 * 128;
 }
 // Steps that a buffer has room for (16 at most: a warp copies the scales of a chunk at once).
 __host__ __device__ constexpr int x_steps_of(int bytes, bool x8, int tile, int rows, int group) {
@@ -102,10 +102,13 @@ __host__ __device__ constexpr int sum_bytes(int nt, int split, int cluster) {
   return (cluster > 1 && pairs < kHandOver ? kHandOver : pairs) * 8 * nt * 32 * 4;
 }
 
-// What `rest` items take on n blocks (or clusters) when each is cut into 2^cut units, in half
-// steps: the rounds of units times the unit's steps and half a step beside them.
-__host__ __device__ __forceinline__ int64_t cost_of(int64_t rest, int n, int steps, int cut) {
-  return ((rest << cut) + n - 1) / n * (((steps + (1 << cut) - 1) >> cut) * 2 + 1);
+// What `rest` < n items take on n blocks (or clusters) when each is cut into 2^cut units, in half
+// steps: the rounds of units times the unit's steps and half a step beside them.  Where a chunk of
+// input rows (x_steps) is less than kDepth steps for a share, every step waits for its rows, and
+// counts one and a half.
+__host__ __device__ __forceinline__ int cost_of(int rest, int n, int steps, int x_steps, int cut) {
+  const int mine = (steps + (1 << cut) - 1) >> cut, chunk = x_steps >> cut;
+  return ((rest << cut) + n - 1) / n * (mine * (chunk < kDepth && chunk < mine ? 3 : 2) + 1);
 }
 
 // Asynchronous copies to shared memory.
@@ -185,13 +188,13 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
           "f"(c[2]), "f"(c[3]));
 }
 
-// The four A registers of one word of codes: the codes as subnormal numbers, those of rows g + 8
-// 16 times as large.
+// The four A registers of one word of codes, as subnormal numbers: in the fragment's rows g the
+// code of row g and 16 times that of row g + 8, in its rows g + 8 the code of row g alone.
 __device__ __forceinline__ void widen(uint32_t w, uint32_t (&a)[4]) {
-  a[0] = w & 0x000f000fu;
-  a[1] = w & 0x00f000f0u;
-  a[2] = (w >> 8) & 0x000f000fu;
-  a[3] = (w >> 8) & 0x00f000f0u;
+  a[0] = w & 0x00ff00ffu;
+  a[1] = w & 0x000f000fu;
+  a[2] = __byte_perm(w, 0, 0x4341);
+  a[3] = a[2] & 0x000f000fu;
 }
 // What makes codes of them again, for rows g and rows g + 8.
 template <bool kX8>
@@ -210,7 +213,7 @@ struct Item {
   int steps = 0;               // of 256 columns, of the longest share
   int x_steps = 0;             // steps (of all shares together) of a chunk of input rows
   bool shared = false;
-  int64_t in_row0 = 0, out_row0 = 0;
+  int in_row0 = 0, out_row0 = 0;  // (rows are below 2^31: checked on the host)
 };
 
 template <int kNt, bool kX8, int kGroup, bool kCluster>
@@ -218,12 +221,15 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
   constexpr int kTile = 8 * kNt;        // rows of a group that one item takes
   constexpr int kSteps = 256 / kGroup;  // groups in a step
   constexpr int kEl = kX8 ? 1 : 2;      // bytes of an input element
-  __shared__ int32_t s_first[kMaxGroups + 1];  // first tile of each group
   __shared__ int32_t s_warp[kWarps];
-  extern __shared__ __align__(16) char s_ring[];  // the rings, two buffers of rows
+  __shared__ int32_t s_x_steps[kTile + 1];     // steps of a chunk of so many rows
+  extern __shared__ __align__(1024) char s_ring[];  // the rings, the rows' buffers, partial sums
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int n_all = a.n_groups + a.has_shared;
+  int32_t* const s_first = reinterpret_cast<int32_t*>(s_ring + a.tables);  // first tiles of groups
+  int32_t* const s_row = s_first + n_all + 1;                              // their first rows
+  int32_t* const s_rows = s_row + n_all;                                   // and their rows
   __shared__ uint64_t s_full[kBuffers], s_free[kBuffers];
   __shared__ int s_abort;
   if (threadIdx.x == 0) {
@@ -236,19 +242,25 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
   }
   pdl_wait();
 
-  auto group_range = [&](int e, int64_t& first, int64_t& n) {
-    if (e >= a.n_groups) {
-      first = 0;
-      n = a.shared_rows;
-    } else if (a.offsets == nullptr) {
-      first = 0;
-      n = a.max_rows;
-    } else {
-      first = a.offsets[e];
-      n = a.offsets[e + 1] - first;
-      if (first < 0 || n < 0 || n > a.max_group_rows || first + n > a.max_rows) n = -1;
-    }
+  // rows of group e, the first of them in `first`; -1 where its offsets are wrong
+  auto group_rows = [&](int e, int& first) -> int {
+    first = 0;
+    if (e >= a.n_groups) return a.shared_rows;
+    if (a.offsets == nullptr) return a.max_rows;
+    first = a.offsets[e];
+    const int64_t n = (int64_t)a.offsets[e + 1] - first;
+    return first < 0 || n < 0 || n > a.max_group_rows || first + n > a.max_rows ? -1 : (int)n;
   };
+  // a row index out of range somewhere: each tile looks for it then
+  bool bad_index = false;
+  if (a.row_index != nullptr) {
+    const int n = a.offsets != nullptr ? min(max(a.offsets[a.n_groups], 0), a.max_rows) : a.max_rows;
+    if (n > 16 * kThreads) bad_index = true;  // (longer than it is worth: they look anyway)
+    for (int i = threadIdx.x; i < n && !bad_index; i += kThreads) {
+      const int v = a.row_index[i];
+      if (v < 0 || v >= a.x_rows) bad_index = true;
+    }
+  }
   {
     // tiles of every group, and their exclusive scan
     const int per = (n_all + kThreads - 1) / kThreads;
@@ -256,14 +268,17 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
     int mine = 0;
     bool bad = false;
     for (int e = e0; e < e0 + per && e < n_all; ++e) {
-      int64_t first, n;
-      group_range(e, first, n);
+      int first, n = group_rows(e, first);
       if (n < 0) bad = true, n = 0;
-      const int tiles = (int)((n + kTile - 1) / kTile);
+      const int tiles = (n + kTile - 1) / kTile;
       s_first[e] = tiles;
+      s_row[e] = first;
+      s_rows[e] = n;
       mine += tiles;
     }
     if (bad && blockIdx.x == 0) report_status(a.status, kStatusInvalidInput);
+    if (threadIdx.x >= 1 && threadIdx.x <= kTile)
+      s_x_steps[threadIdx.x] = x_steps_of(a.buf_bytes, kX8, kTile, threadIdx.x, kGroup);
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -280,14 +295,14 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
       at += tiles;
     }
     if (threadIdx.x == kThreads - 1) s_first[n_all] = at;
-    __syncthreads();
+    bad_index = __syncthreads_or(bad_index);
   }
   // The blocks of a cluster work on the same items, each on its run of the steps, k0 onwards.
   const int per = kCluster ? a.cluster : 1, all_steps = (a.ku + 3) / 4, rank = blockIdx.x % per;
   const int k0 = all_steps * rank / per;
   const int n_steps = all_steps * (rank + 1) / per - k0;
-  // an item: a tile and a pair of blocks for each warp; those after the last whole round of the blocks are
-  // cut into 2^cut units
+  // an item: a tile and a pair of blocks for each warp; those after the last whole round of the
+  // blocks are cut into 2^cut units
   const int chunks = (a.pairs + kWarps - 1) / kWarps;
   const int n_blocks = (int)gridDim.x / per, block = (int)blockIdx.x / per;
   const int items = s_first[n_all] * chunks;  // (units are below 2^31: checked on the host)
@@ -295,7 +310,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
   int cut = 0;
   for (int c = 1; 1 << c <= a.max_split; ++c) {
     const int most = (all_steps + per - 1) / per;  // (the cut is all blocks' alike)
-    if (cost_of(rest, n_blocks, most, c) < cost_of(rest, n_blocks, most, cut)) cut = c;
+    if (cost_of(rest, n_blocks, most, a.x_steps, c) < cost_of(rest, n_blocks, most, a.x_steps, cut))
+      cut = c;
   }
   const int units = whole + (rest << cut);
 
@@ -320,20 +336,17 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
       else
         hi = mid;
     }
-    int64_t first, n;
-    group_range(r.e, first, n);
-    const int64_t row0 = (int64_t)(tile - s_first[r.e]) * kTile;
-    r.tile_rows = (int)min((int64_t)kTile, n - row0);
-    r.x_steps = min(x_steps_of(a.buf_bytes, kX8, kTile, r.tile_rows, kGroup), n_steps + r.split - 1) >>
-                r.log2 << r.log2;
     r.shared = r.e >= a.n_groups;
+    const int first = s_row[r.e], row0 = (tile - s_first[r.e]) * kTile;
+    r.tile_rows = min(kTile, s_rows[r.e] - row0);
+    r.x_steps = min(s_x_steps[r.tile_rows], n_steps + r.split - 1) >> r.log2 << r.log2;
     r.out_row0 = (r.shared ? a.shared_out_row0 : first) + row0;
     r.in_row0 = (r.shared ? a.shared_x_row0 : first) + row0;
     return r;
   };
   // the input row of a tile's row r; -1 where its index is out of range
-  auto row_of = [&](const Item& im, int r) -> int64_t {
-    int64_t v = im.in_row0 + r;
+  auto row_of = [&](const Item& im, int r) -> int {
+    int v = im.in_row0 + r;
     if (!im.shared && a.row_index != nullptr) v = a.row_index[v];
     return v < 0 || v >= a.x_rows ? -1 : v;
   };
@@ -368,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
       c_x_steps = im.x_steps;
       c_over = 1 << (32 - __clz(c_rows - 1));
       const int r = min(warp & (c_over - 1), c_rows - 1);
-      const int64_t row = max(row_of(im, r), (int64_t)0);
+      const int64_t row = max(row_of(im, r), 0);
       c_x = static_cast<const char*>(a.x) + (row * a.cols + 256 * k0 + 8 * lane) * kEl;
       c_xs = kX8 ? a.x_scale + row * a.xs_ld + (2 * k0 + lane) * a.xs_step : nullptr;
     }
@@ -572,10 +585,10 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
                 for (int n = 0; n < kN; ++n) {
                   const float2 o = *reinterpret_cast<const float2*>(
                       po + (h / (kGroup / 32) * kTile + 8 * n) * 4);
-                  off[n][0] = o.x;
-                  off[n][1] = o.y;
-                  off[n][2] = 16.f * o.x;
-                  off[n][3] = 16.f * o.y;
+                  off[n][0] = 17.f * o.x;
+                  off[n][1] = 17.f * o.y;
+                  off[n][2] = o.x;
+                  off[n][3] = o.y;
                 }
               }
 #pragma unroll
@@ -599,17 +612,20 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
                 const float lo = __uint_as_float(sw << 16), up = __uint_as_float(sw & 0xffff0000u);
 #pragma unroll
                 for (int n = 0; n < kN; ++n) {
+                  // rows g, then rows g + 8 (16 times as large)
+                  const float s0 = part[m][n][2], s1 = part[m][n][3];
+                  const float s2 = part[m][n][0] - s0, s3 = part[m][n][1] - s1;
                   if (kX8) {
                     const float2 xs = *reinterpret_cast<const float2*>(pxs + (h / 4 * kTile + 8 * n) * 4);
-                    acc[m][n][0] = fmaf(part[m][n][0], lo * xs.x, acc[m][n][0]);
-                    acc[m][n][1] = fmaf(part[m][n][1], lo * xs.y, acc[m][n][1]);
-                    acc[m][n][2] = fmaf(part[m][n][2], up * xs.x, acc[m][n][2]);
-                    acc[m][n][3] = fmaf(part[m][n][3], up * xs.y, acc[m][n][3]);
+                    acc[m][n][0] = fmaf(s0, lo * xs.x, acc[m][n][0]);
+                    acc[m][n][1] = fmaf(s1, lo * xs.y, acc[m][n][1]);
+                    acc[m][n][2] = fmaf(s2, up * xs.x, acc[m][n][2]);
+                    acc[m][n][3] = fmaf(s3, up * xs.y, acc[m][n][3]);
                   } else {
-                    acc[m][n][0] = fmaf(part[m][n][0], lo, acc[m][n][0]);
-                    acc[m][n][1] = fmaf(part[m][n][1], lo, acc[m][n][1]);
-                    acc[m][n][2] = fmaf(part[m][n][2], up, acc[m][n][2]);
-                    acc[m][n][3] = fmaf(part[m][n][3], up, acc[m][n][3]);
+                    acc[m][n][0] = fmaf(s0, lo, acc[m][n][0]);
+                    acc[m][n][1] = fmaf(s1, lo, acc[m][n][1]);
+                    acc[m][n][2] = fmaf(s2, up, acc[m][n][2]);
+                    acc[m][n][3] = fmaf(s3, up, acc[m][n][3]);
                   }
                 }
               }
@@ -708,40 +724,51 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
       if (rank != 0) continue;
     }
     if (dead || n_mine == 0 || ks != 0) continue;
+    // rows 16 b + g and + 8 of block b, and (without SwiGLU) of the block behind it
+    const int row0 = 16 * (a.parts == 2 ? pair : 2 * pair) + g;
 #pragma unroll
     for (int n = 0; n < kNt; ++n) {
+      if (8 * n >= im.tile_rows) break;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int r = 8 * n + 2 * t + j;
         if (r >= im.tile_rows) continue;
-        // a row index out of range is reported, and its row reads as zeros
-        const bool known = row_of(im, r) >= 0;
-        if (!known) report_status(a.status, kStatusInvalidInput);
-        const int64_t o = (im.out_row0 + r) * a.rows;
+        float v[2][2];  // [block][row]
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int m = q >> 1, i = (q & 1) * 2 + j;  // block, and row g or g + 8 of it
-          if (a.parts == 2 && m == 1) continue;
-          const float u = code_unit<kX8>(q & 1);
-          float v = acc[m][n][i] * u;
-          const int b = a.parts == 2 ? pair : 2 * pair + m;
-          if (a.parts == 2) {
-            float up = acc[1][n][i] * u;
+        for (int m = 0; m < 2; ++m) {
+          v[m][0] = acc[m][n][j] * code_unit<kX8>(false);
+          v[m][1] = acc[m][n][2 + j] * code_unit<kX8>(true);
+        }
+        if (a.parts == 2) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            float gate = v[0][q], up = v[1][q];
             if (a.clamp > 0.f) {
-              v = clip(v, a.clamp);
+              gate = clip(gate, a.clamp);
               up = clip(up, a.clamp);
             }
-            v = v / (1.f + expf(-v)) * up;
-          } else if (a.relu) {
-            v = v < 0.f ? 0.f : v;
+            v[0][q] = gate / (1.f + expf(-gate)) * up;
           }
-          if (!known) v = 0.f;
-          const int row = 16 * b + g + 8 * (q & 1);
-          if (row >= a.rows) continue;
+        } else if (a.relu) {
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) v[m][q] = v[m][q] < 0.f ? 0.f : v[m][q];
+        }
+        // a row index out of range is reported, and its row reads as zeros
+        if (bad_index && row_of(im, r) < 0) {
+          report_status(a.status, kStatusInvalidInput);
+          v[0][0] = v[0][1] = v[1][0] = v[1][1] = 0.f;
+        }
+        const int64_t o = (int64_t)(im.out_row0 + r) * a.rows + row0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (a.parts == 2 && q >= 2) break;
+          if (row0 + 8 * q >= a.rows) break;
           if (a.out_f32)
-            static_cast<float*>(a.out)[o + row] = v;
+            static_cast<float*>(a.out)[o + 8 * q] = v[q >> 1][q & 1];
           else
-            static_cast<__nv_bfloat16*>(a.out)[o + row] = __float2bfloat16_rn(v);
+            static_cast<__nv_bfloat16*>(a.out)[o + 8 * q] = __float2bfloat16_rn(v[q >> 1][q & 1]);
         }
       }
     }
@@ -870,16 +897,16 @@ cudaError_t launch_w4(const W4Gemm& p, cudaStream_t stream, int* launches) {
   a.x_scale = p.x_scale;
   a.xs_step = p.x_group != 0;
   a.xs_ld = p.x_group != 0 ? (p.cols + 127) / 128 : 1;
-  a.x_rows = p.x_rows;
+  a.x_rows = (int)p.x_rows;
   a.row_index = p.row_index;
   a.offsets = p.offsets;
   a.n_groups = p.n_groups;
   a.has_shared = p.has_shared;
-  a.max_rows = p.max_rows;
-  a.max_group_rows = p.max_group_rows;
-  a.shared_rows = p.shared_rows;
-  a.shared_x_row0 = p.shared_x_row0;
-  a.shared_out_row0 = p.shared_out_row0;
+  a.max_rows = (int)p.max_rows;
+  a.max_group_rows = (int)p.max_group_rows;
+  a.shared_rows = (int)p.shared_rows;
+  a.shared_x_row0 = (int)p.shared_x_row0;
+  a.shared_out_row0 = (int)p.shared_out_row0;
   a.pairs = p.parts == 2 ? a.rb : (a.rb + 1) / 2;
   a.relu = p.relu;
   a.clamp = p.clamp;
@@ -896,21 +923,16 @@ cudaError_t launch_w4(const W4Gemm& p, cudaStream_t stream, int* launches) {
   const int rows = (int)(most < tile ? most : tile);  // the most of a tile
   // shared memory: the rings, the partial sums, and three buffers of input rows, in which a
   // chunk of a step for each share of a cut item has to fit
+  const int table_bytes = 4 * (3 * (p.n_groups + p.has_shared) + 1);
   const auto buffer = [&](int split, int cluster) {
-    const int room = (kDynamicSmem - kWarps * kDepth * kStep -
-                      sum_bytes(nt, split, cluster)) / kBuffers / 16 * 16;
+    const int room = (kDynamicSmem - table_bytes - kWarps * kDepth * kStep -
+                      sum_bytes(nt, split, cluster)) / kBuffers / 128 * 128;
     const int all = x_bytes(x8, tile, rows, n_steps < 16 ? n_steps : 16, p.group);
     return room < all ? room : all;
   };
-  const auto max_split = [&](int cluster) {
-    int split = 1;
-    while (split < kWarps && 2 * split * cluster <= n_steps &&
-           x_steps_of(buffer(2 * split, cluster), x8, tile, rows, p.group) >= 2 * split)
-      split *= 2;
-    return split;
-  };
-  // Clusters of 1, 2, 4 or 8 blocks (of 8, two to each of the device's eight clusters of SMs),
-  // whichever has the items that are expected done first; a unit's hand-over takes about a step.
+  // Clusters of 1, 2, 4 or 8 blocks (of 8, two to each of the device's eight clusters of SMs), and
+  // the finest cut that there is room for, whichever has the items that are expected done first;
+  // a unit's hand-over takes about a step.
   const int64_t shared_tiles = p.has_shared ? (p.shared_rows + tile - 1) / tile : 0;
   const int64_t reached = p.max_rows < p.n_groups ? p.max_rows : p.n_groups;
   const int64_t chunks = (a.pairs + kWarps - 1) / kWarps;
@@ -920,22 +942,31 @@ cudaError_t launch_w4(const W4Gemm& p, cudaStream_t stream, int* launches) {
   int64_t least = -1;
   for (int c = 1; c <= 8 && c <= n_steps && c <= sms; c *= 2) {
     const int n = clusters_of(c), steps = (n_steps + c - 1) / c;
-    int64_t rest = cost_of(expected % n, n, steps, 0);
-    for (int k = 1; 1 << k <= max_split(c); ++k)
-      rest = std::min(rest, cost_of(expected % n, n, steps, k));
-    const int64_t cost = expected / n * (2 * steps + 1) + rest +
-                         (c > 1 ? (expected + n - 1) / n * 2 : 0);
-    if (least < 0 || cost < least) least = cost, a.cluster = c;
+    int rest = INT32_MAX;
+    for (int k = 0; 1 << k <= kWarps && 1 << k <= steps; ++k) {
+      const int x_steps = x_steps_of(buffer(1 << k, c), x8, tile, rows, p.group);
+      if (x_steps < 1 << k) break;
+      for (int cut = 0; cut <= k; ++cut)
+        rest = std::min(rest, cost_of((int)(expected % n), n, steps, x_steps, cut));
+      const int64_t cost = expected / n * cost_of(1, 1, steps, x_steps, 0) + rest +
+                           (c > 1 ? (expected + n - 1) / n * 2 : 0);
+      if (least < 0 || cost < least) {
+        least = cost;
+        a.cluster = c;
+        a.max_split = 1 << k;
+        a.x_steps = x_steps;
+      }
+    }
   }
-  a.max_split = max_split(a.cluster);
   a.buf_bytes = buffer(a.max_split, a.cluster);
   const int64_t tiles = p.max_rows / tile + reached + shared_tiles;
   const int64_t units = tiles * chunks * a.max_split;
   if (units > INT32_MAX) return cudaErrorInvalidValue;
   const int64_t n = clusters_of(a.cluster);
   const int grid = (int)(units < 1 ? 1 : units < n ? units : n) * a.cluster;
-  const size_t bytes = (size_t)kWarps * kDepth * kStep +
-                       sum_bytes(nt, a.max_split, a.cluster) + kBuffers * (size_t)a.buf_bytes;
+  a.tables = kWarps * kDepth * kStep + sum_bytes(nt, a.max_split, a.cluster) +
+             kBuffers * a.buf_bytes;
+  const size_t bytes = (size_t)a.tables + table_bytes;
   ++*launches;
   return x8 ? launch_tile<true>(a, nt, p.group, grid, bytes, stream)
             : launch_tile<false>(a, nt, p.group, grid, bytes, stream);
