@@ -346,6 +346,8 @@ MOE_API moe_status moe_w4_quantize(const moe_w4* w, const void* W, moe_stream_t 
 
 /* out[r] = W_e x[r] for the rows r of each group (parts = 1), or SiLU(clamp(gate_e x[r])) *
  * clamp(up_e x[r]) (parts = 2).  Products are exact and sums are fp32; out is rounded once.
+ * The sums of a row keep their full accuracy while its largest products are above 2^-57; bf16
+ * values of 2^63 and more count as infinite.
  *   x        bf16 [x_rows][cols], or with x_scale e4m3 [x_rows][cols]: x_scale fp32
  *            [x_rows][ceil(cols / 128)] (x_group = 128) or [x_rows][1] (x_group = 0), the two
  *            8-bit outputs of moe_rms_norm
@@ -356,7 +358,9 @@ MOE_API moe_status moe_w4_quantize(const moe_w4* w, const void* W, moe_stream_t 
  *   out      [rows][w->rows], out_dtype MOE_DT_BF16 or MOE_DT_F32
  *   ws       NULL, or a workspace whose status word records offsets or row indices out of range
  *            (MOE_ERR_INVALID_INPUT; such a group is skipped, such a row reads zeros)
- * Meant for decode: weights are read once for every 32 rows of a group. */
+ * Meant for decode: weights are read once for every 16 rows of a group.  The result depends on
+ * the inputs and sizes alone, not on the order of execution; the same row may give other last
+ * bits in a batch of another size. */
 MOE_API moe_status moe_w4_matmul(const moe_w4* w, const void* x, const float* x_scale,
                                  int32_t x_group, int64_t x_rows, const int32_t* offsets,
                                  const int32_t* row_index, int64_t rows, float clamp, void* out,
@@ -365,7 +369,8 @@ MOE_API moe_status moe_w4_matmul(const moe_w4* w, const void* x, const float* x_
 /* moe_expert_ffn with 4-bit weights (bf16 layers): ye[r] = FFN_e(x[row_token[r]]) for r in
  * [offsets[e], offsets[e+1]), and ye[N*k + t] = FFN_shared(x[t]) when n_shared == 1.
  *   x [N][d] bf16, or e4m3 with x_scale [N][ceil(d / 128)] (moe_rms_norm's, group 128)
- *   offsets [E+1], row_token [N*k]: as written by moe_permute (no gathered rows are needed)
+ *   offsets [E+1], row_token [N*k]: as written by moe_permute (no gathered rows are needed); a
+ *   group has at most N rows (a longer one is skipped and reported as MOE_ERR_INVALID_INPUT)
  *   W_gu: mats = E + S, parts = 2 (SwiGLU) or 1 (ReLU), rows = F, cols = d
  *   W_down: mats = E + S, parts = 1, rows = d, cols = F
  *   ye [N*k + S*N][d] bf16.  Hidden activations are rounded to bf16 in the workspace, as in

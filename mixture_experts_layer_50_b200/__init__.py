@@ -3,7 +3,9 @@
 The layer runs in ``libmoe_b200.so`` (C ABI in ``include/moe.h``).  This package is the
 thin Python binding: ``moe_route``, ``moe_permute``, ``moe_expert_ffn``, ``moe_combine``,
 ``moe_forward`` and ``moe_forward_host`` keep the C names and take torch CUDA tensors;
-``MoELayer`` bundles a layer's weights and workspace; ``EPMoELayer`` is one rank of the
+``MoELayer`` bundles a layer's weights and workspace, ``W4MoELayer`` one whose experts are held
+in 4 bits; ``moe_rms_norm``, ``moe_w4_matmul`` and ``moe_balance_loss`` are the operators around
+the router and the experts; ``EPMoELayer`` is one rank of the
 expert-parallel layer (experts spread over the ranks of a process group).  Accessing any of them loads the
 library and raises ``ImportError`` if it has not been built -- there is no fallback.
 """
@@ -33,8 +35,8 @@ def __getattr__(name):
         value = getattr(importlib.import_module("._native", __name__), name)
         globals()[name] = value  # looked up once
         return value
-    if name == "MoELayer":
-        return importlib.import_module(".layer", __name__).MoELayer
+    if name in ("MoELayer", "W4MoELayer"):
+        return getattr(importlib.import_module(".layer", __name__), name)
     if name == "EPMoELayer":
         return importlib.import_module(".ep", __name__).EPMoELayer
     raise AttributeError(name)

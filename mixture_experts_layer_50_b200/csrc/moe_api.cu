@@ -792,6 +792,15 @@ moe::W4Gemm w4_gemm(const moe_w4& w) {
   return p;
 }
 
+// The kernel numbers its units of work in 32 bits.
+moe_status check_w4_size(const moe::W4Gemm& p) {
+  const int64_t tiles = p.max_rows / 8 + std::min<int64_t>(p.max_rows, p.n_groups) +
+                        (p.shared_rows + 7) / 8;
+  if (tiles * (p.rows / 256 + 1) > INT32_MAX / 16)
+    return fail(MOE_ERR_UNSUPPORTED, "too many rows times outputs for one 4-bit product");
+  return MOE_OK;
+}
+
 // The two products of the experts; the routed rows are read through row_token, so no gathered
 // copy of them is made.
 moe_status stage_ffn_w4(const moe_config& c, const Ws& L, void* ws, const void* x,
@@ -818,8 +827,6 @@ moe_status stage_ffn_w4(const moe_config& c, const Ws& L, void* ws, const void* 
   p.clamp = c.clamp;
   p.out = at<char>(ws, L.h);
   p.status = at<int>(ws, L.status);
-  MOE_CUDA(moe::launch_w4(p, st, launches), "4-bit gate/up product");
-  prof_mark(st);
   moe::W4Gemm r = w4_gemm(down);
   r.x = at<char>(ws, L.h);
   r.x_rows = Nk + c.n_shared * c.N;
@@ -833,6 +840,10 @@ moe_status stage_ffn_w4(const moe_config& c, const Ws& L, void* ws, const void* 
   r.shared_out_row0 = Nk;
   r.out = ye;
   r.status = p.status;
+  MOE_TRY(check_w4_size(p));
+  MOE_TRY(check_w4_size(r));
+  MOE_CUDA(moe::launch_w4(p, st, launches), "4-bit gate/up product");
+  prof_mark(st);
   MOE_CUDA(moe::launch_w4(r, st, launches), "4-bit down product");
   prof_mark(st);
   return MOE_OK;
@@ -1309,6 +1320,7 @@ moe_status moe_w4_matmul(const moe_w4* w, const void* x, const float* x_scale, i
   p.out = out;
   p.out_f32 = out_dtype == MOE_DT_F32;
   p.status = static_cast<int*>(ws);
+  MOE_TRY(check_w4_size(p));
   int launches = 0;
   MOE_CUDA(moe::launch_w4(p, (cudaStream_t)stream, &launches), "4-bit product");
   g_last_launches = launches;

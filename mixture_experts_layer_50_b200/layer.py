@@ -80,7 +80,7 @@ class MoELayer:
         N = x_host.shape[0]
         st = torch.cuda.current_stream() if stream is None else stream
         with torch.cuda.stream(st):
-            xd = torch.empty(x_host.shape, dtype=x_host.dtype, device=self.W_gu.device)
+            xd = torch.empty(x_host.shape, dtype=x_host.dtype, device=self.W_g.device)
             xd.copy_(x_host, non_blocking=True)
             y = self.forward(xd, modality=modality, stream=st)
             y_host[:N].copy_(y, non_blocking=True)
@@ -137,3 +137,84 @@ class MoELayer:
 
     def check_status(self, stream=None) -> int:
         return nat.moe_check_status(self.ws, stream)
+
+
+class W4MoELayer(MoELayer):
+    """A bf16 layer whose expert weights are held in 4 bits (``moe_forward_w4``), for decode.
+
+    ``W_gu`` and ``W_down`` are ``nat.W4Matrix``; ``from_layer`` quantises a ``MoELayer``'s.  The
+    router and everything else are the layer's own.  ``forward_normed`` puts the residual RMS
+    norm before it and hands the experts the norm's 8-bit rows.
+    """
+
+    def __init__(self, *, W_g, W_gu, W_down, k, n_shared=0, score_fn=nat.SOFTMAX, renorm=1,
+                 act=nat.SWIGLU, clamp=0.0, bias=None, logit_offset=None, capacity_factor=None,
+                 max_tokens: int):
+        self.overflow = "drop"
+        self.W_g, self.W_gu, self.W_down = W_g, W_gu, W_down
+        self.E, self.d = W_g.shape
+        self.F = W_down.cols
+        self.k, self.n_shared = k, n_shared
+        self.score_fn, self.renorm, self.act, self.clamp = score_fn, renorm, act, clamp
+        self.bias, self.logit_offset = bias, logit_offset
+        self.n_bias_sets = 0 if bias is None else bias.shape[0]
+        self.capacity_factor = capacity_factor
+        self.dtype = nat.BF16
+        self.max_tokens = max_tokens
+        self.ws = nat.alloc_workspace(self.config(max_tokens), device=W_g.device)
+        self._graphs = {}
+
+    @classmethod
+    def from_layer(cls, layer: MoELayer, group: int = 128, max_tokens: Optional[int] = None):
+        if layer.overflow != "drop":
+            raise ValueError("4-bit layers have the 'drop' overflow policy only")
+        if layer.dtype != nat.BF16:
+            raise ValueError("4-bit experts need a bf16 layer")
+        parts = 2 if layer.act == nat.SWIGLU else 1
+        return cls(W_g=layer.W_g, W_gu=nat.W4Matrix.quantize(layer.W_gu, parts=parts, group=group),
+                   W_down=nat.W4Matrix.quantize(layer.W_down, group=group), k=layer.k,
+                   n_shared=layer.n_shared, score_fn=layer.score_fn, renorm=layer.renorm,
+                   act=layer.act, clamp=layer.clamp, bias=layer.bias,
+                   logit_offset=layer.logit_offset, capacity_factor=layer.capacity_factor,
+                   max_tokens=layer.max_tokens if max_tokens is None else max_tokens)
+
+    def forward(self, x: torch.Tensor, modality=None, y=None, route_out: Optional[dict] = None,
+                stream=None, x8=None, x8_scale=None) -> torch.Tensor:
+        N = x.shape[0]
+        self._check_tokens(N)
+        if y is None:
+            y = torch.empty_like(x)
+        nat.moe_forward_w4(self.config(N), x=x, x8=x8, x8_scale=x8_scale, W_g=self.W_g,
+                           W_gu=self.W_gu, W_down=self.W_down, y=y,
+                           logit_offset=self.logit_offset, bias=self.bias, modality=modality,
+                           route_out=route_out, ws=self.ws, stream=stream)
+        return y
+
+    def forward_normed(self, x: torch.Tensor, residual: torch.Tensor, weight=None,
+                       eps: float = 1e-6, modality=None, route_out: Optional[dict] = None,
+                       stream=None):
+        """The layer of RMS norm(x + residual) * weight; returns (y, x + residual)."""
+        N, d = x.shape
+        h, total = torch.empty_like(x), torch.empty_like(x)
+        h8 = torch.empty((N, d), dtype=torch.float8_e4m3fn, device=x.device)
+        h8_scale = torch.empty((N, (d + 127) // 128), device=x.device)
+        nat.moe_rms_norm(x=x, residual=residual, weight=weight, eps=eps, y=h, residual_out=total,
+                         y8=h8, y8_scale=h8_scale, stream=stream)
+        y = self.forward(h, modality=modality, route_out=route_out, stream=stream, x8=h8,
+                         x8_scale=h8_scale)
+        if isinstance(stream, torch.cuda.Stream):
+            for t in (x, residual, h, total, h8, h8_scale, y):
+                t.record_stream(stream)
+        return y, total
+
+    def forward_host(self, x_host: torch.Tensor, y_host: torch.Tensor, modality=None,
+                     stream=None) -> torch.Tensor:
+        self._check_tokens(x_host.shape[0])
+        return self._forward_host_copies(x_host, y_host, modality, stream, sync=True)
+
+    def forward_host_batches(self, x_host: list, y_host: list, modality=None, stream=None):
+        self._check_tokens(x_host[0].shape[0])
+        for xb, yb in zip(x_host, y_host):
+            self._forward_host_copies(xb, yb, modality, stream, sync=False)
+        (torch.cuda.current_stream() if stream is None else stream).synchronize()
+        return y_host

@@ -391,3 +391,145 @@ def test_empty_batch():
                           W_down=dn, ye=e, ws=ws)
     one, _ = make_w(1, 1, 64, 64, 64, seed=3)
     nat.moe_w4_matmul(one, x=e, out=torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"))
+
+
+def values_on_gpu(w):
+    """R.w4_values in float64 on the device, for the large shapes."""
+    r, c = torch.arange(w.rows, device="cuda")[:, None], torch.arange(w.cols, device="cuda")[None]
+    byte = 16 * (4 * (r % 8) + c % 32 // 8) + 4 * (2 * (c % 64 // 32) + c % 8 // 4) + 2 * (c % 2) + c % 4 // 2
+    both = w.q[:, :, r // 16, c // 64, byte]
+    code = torch.where(r % 16 < 8, both & 15, both >> 4).double()
+    return (code - 8) * w.scale[:, :, r // 16, c // w.group, r % 8, r % 16 // 8].double()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,rows,cols,parts,group", [
+    (1, 7176, 2056, 2, 128),      # whole rounds of items and a cut rest
+    (3, 2064, 14336, 1, 64),      # few items, many columns: clusters
+    (9, 520, 8200, 1, 32),        # a cluster whose last run is ragged
+    (16, 4104, 1800, 2, 64),
+    (33, 1032, 7176, 1, 128),     # three tiles
+    (48, 264, 4360, 2, 32),
+    (200, 512, 1160, 1, 64),      # thirteen tiles
+    (2, 48, 264, 1, 32)])
+def test_large_shapes(n, rows, cols, parts, group, kind):
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    shape = (1, parts, -(-rows // 16))
+    q = torch.randint(0, 256, shape + (-(-cols // 64), 512), generator=g, device="cuda", dtype=torch.uint8)
+    sc = (torch.rand(shape + (-(-cols // group), 8, 2), generator=g, device="cuda") * 0.02 + 0.01).to(torch.bfloat16)
+    w = nat.W4Matrix(q, sc, rows=rows, cols=cols, group=group)
+    x, xs, xg, xv = make_x(n, cols, kind, seed=n)
+    wv, xt = values_on_gpu(w)[0], torch.from_numpy(xv).cuda()
+    z = [xt @ m.t() for m in wv]
+    t = [(group / 16 + (cols / group + 12 + 8) / 4) * 2.0 ** -22 * (xt.abs() @ m.abs().t()) for m in wv]
+    if parts == 2:
+        s = z[0] * torch.sigmoid(z[0])
+        v = s * z[1]
+        tol = 1.1 * (z[1].abs() + t[1]) * t[0] + (s.abs() + t[0]) * t[1] + 2.0 ** -20 * v.abs()
+    else:
+        v, tol = z[0], t[0]
+    out = [torch.empty(n, rows, device="cuda") for _ in range(2)]
+    for o in out:
+        nat.moe_w4_matmul(w, x=x, x_scale=xs, x_group=xg, out=o)
+    assert torch.equal(out[0].view(torch.int32), out[1].view(torch.int32))      # the same bits again
+    assert within(f64(out[0]), v.cpu().numpy(), (tol + v.abs() * 2.0 ** -24 + 1e-37).cpu().numpy())
+
+
+@pytest.mark.parametrize("N,E,k,S,C", [(1, 64, 8, 1, 0), (24, 40, 4, 1, 0), (90, 5, 2, 0, 30), (300, 9, 2, 1, 0)])
+def test_large_ffn_against_the_bf16_layer(N, E, k, S, C):
+    """Many groups, tiles and units: the 4-bit experts against the bf16 experts on the values that
+    the codes stand for (those of multiples of 2^-7 up to 7 are bf16 numbers)."""
+    d, F = 1032, 520
+    g = torch.Generator(device="cuda").manual_seed(N)
+    codes = [torch.randint(-7, 8, s, generator=g, device="cuda").to(torch.bfloat16)
+             for s in ((E + S, 2 * F, d), (E + S, d, F))]
+    for c in codes:
+        c[..., ::32] = 7
+    Wgu, Wdn = (c * 2.0 ** -7 for c in codes)
+    cfg = nat.make_config(N, d, E, k, F, n_shared=S, capacity=C)
+    x = torch.randn(N, d, generator=g, device="cuda").to(torch.bfloat16)
+    z = torch.randn(N, E, generator=g, device="cuda")
+    ws = nat.alloc_workspace(cfg)
+    ids, gates = torch.empty(N, k, dtype=torch.int32, device="cuda"), torch.empty(N, k, device="cuda")
+    counts, demand = (torch.empty(E, dtype=torch.int32, device="cuda") for _ in range(2))
+    drop = torch.empty(N, k, dtype=torch.uint8, device="cuda")
+    nat.moe_route(cfg, logits=z, ids=ids, gates=gates, counts=counts, demand=demand, drop_mask=drop, ws=ws)
+    off = torch.empty(E + 1, dtype=torch.int32, device="cuda")
+    tok, slot = torch.full((N * k,), -7, dtype=torch.int32, device="cuda"), torch.empty(N, k, dtype=torch.int32, device="cuda")
+    xp = torch.empty(N * k, d, dtype=torch.bfloat16, device="cuda")
+    nat.moe_permute(cfg, ids=ids, drop_mask=drop, x=x, offsets=off, row_token=tok, slot_row=slot, xp=xp, ws=ws)
+    ye, y4 = (torch.zeros(N * k + S * N, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    nat.moe_expert_ffn(cfg, xp=xp, offsets=off, x=x, W_gu=Wgu, W_down=Wdn, ye=ye, ws=ws)
+    nat.moe_expert_ffn_w4(cfg, x=x, offsets=off, row_token=tok, W_gu=nat.W4Matrix.quantize(Wgu, parts=2, group=32),
+                          W_down=nat.W4Matrix.quantize(Wdn, group=32), ye=y4, ws=ws)
+    check_status(ws)
+    assert_close_layer(host(y4), host(ye).astype(np.float64))
+
+
+def test_small_and_large_numbers():
+    w, wv = make_w(1, 1, 64, 512, 128, seed=21)
+    x, _, _, xv = make_x(5, 512, "bf16", seed=22)
+    out = torch.empty(5, 64, device="cuda")
+    for e in (-45, 40, 58):
+        nat.moe_w4_matmul(w, x=(x.double() * 2.0 ** e).to(torch.bfloat16), out=out)
+        v, tol = expect(wv[0], xv * 2.0 ** e, 512, 128)
+        assert within(f64(out), v, tol + np.abs(v) * 2.0 ** -24)
+    nat.moe_w4_matmul(w, x=(x.double() * 2.0 ** -100).to(torch.bfloat16), out=out)
+    assert np.abs(f64(out)).max() <= 2.0 ** -75              # nothing but what is left of 2^-100
+    nat.moe_w4_matmul(w, x=torch.full_like(x, 2.0 ** 63), out=out)
+    assert not torch.isfinite(out).any()
+
+
+def test_layer_class():
+    shape = W.PRESETS["dsv3-n64"].replace(N=20, d=256, E=8, k=2, F=128)
+    t = W.make_inputs(shape, device="cuda")
+    from mixture_experts_layer_50_b200 import MoELayer, W4MoELayer
+    layer = MoELayer.from_workload(shape, t)
+    w4 = W4MoELayer.from_layer(layer, group=32)
+    y = w4.forward(t["x"])
+    want = torch.empty_like(y)
+    nat.moe_forward_w4(w4.config(20), x=t["x"], W_g=t["W_g"], W_gu=w4.W_gu, W_down=w4.W_down, y=want, bias=t["bias"],
+                       ws=w4.ws)
+    assert torch.equal(y, want) and w4.check_status() == 0
+    # 4 bits: the largest of 32 normal weights is 7 steps, some 2.2 sigma, so a step is 0.31 sigma
+    # and its rounding 0.09 sigma rms; three matrices in a product: 16 %
+    assert np.sqrt(((host(y) - host(layer.forward(t["x"]))) ** 2).mean()) <= 0.2 * np.sqrt((host(y) ** 2).mean())
+    got = torch.empty_like(y)
+    for _ in range(2):
+        assert torch.equal(w4.forward_graphed(t["x"], got), want)
+    xh, yh = t["x"].cpu().pin_memory(), torch.empty(20, 256, dtype=torch.bfloat16).pin_memory()
+    assert torch.equal(w4.forward_host(xh, yh), want.cpu())
+    res = torch.randn(20, 256, device="cuda").to(torch.bfloat16)
+    yn, total = w4.forward_normed(t["x"], res, weight=torch.ones(256, dtype=torch.bfloat16, device="cuda"))
+    assert torch.equal(total, (t["x"].float() + res.float()).to(torch.bfloat16))
+    h = torch.empty_like(y)
+    nat.moe_rms_norm(x=t["x"], residual=res, y=h)
+    # the same rows in bf16: e4m3 is off by 2^-4 at most, 2.6 % rms, in both factors of SwiGLU
+    bf = w4.forward(h)
+    assert np.sqrt(((host(yn) - host(bf)) ** 2).mean()) <= 0.1 * np.sqrt((host(bf) ** 2).mean())
+    with pytest.raises(ValueError):
+        w4.forward(torch.empty(21, 256, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError):
+        W4MoELayer.from_layer(MoELayer.from_workload(shape, t, overflow="reroute"))
+
+
+def test_two_graphs_share_a_workspace():
+    cases = [ffn_case(n, 256, 128, 5, 2, 1, 64, "bf16", seed=n) for n in (7, 30)]
+    ws = nat.alloc_workspace(cases[1][0])
+    graphs = []
+    for cfg, gu, _, dn, _, x, xs, _, off, tok in cases:
+        a = dict(x=x, x_scale=xs, offsets=dev(off), row_token=dev(tok), W_gu=gu, W_down=dn)
+        want = torch.empty(cfg.N * 3, 256, dtype=torch.bfloat16, device="cuda")
+        nat.moe_expert_ffn_w4(cfg, ye=want, ws=nat.alloc_workspace(cfg), **a)
+        got, g = torch.zeros_like(want), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            nat.moe_expert_ffn_w4(cfg, ye=got, ws=ws, **a)
+        graphs.append((g, got, want, a))
+    for _ in range(3):
+        for g, got, _, _ in graphs:
+            got.zero_()
+            g.replay()
+    torch.cuda.synchronize()
+    for _, got, want, _ in graphs:
+        assert torch.equal(got, want)
