@@ -796,7 +796,7 @@ moe::W4Gemm w4_gemm(const moe_w4& w) {
 moe_status check_w4_size(const moe::W4Gemm& p) {
   const int64_t tiles = p.max_rows / 8 + std::min<int64_t>(p.max_rows, p.n_groups) +
                         (p.shared_rows + 7) / 8;
-  if (tiles * (p.rows / 256 + 1) > INT32_MAX / 16)
+  if (tiles * (p.rows / 256 + 1) > INT32_MAX / 32)
     return fail(MOE_ERR_UNSUPPORTED, "too many rows times outputs for one 4-bit product");
   return MOE_OK;
 }

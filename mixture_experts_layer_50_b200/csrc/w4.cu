@@ -6,38 +6,44 @@
 // of an expert's first projection in the epilogue.
 //
 // Bound: HBM reads of the weights, half a byte each.  An SM has to take about 24 bytes, 49
-// weights, per clock, so the cost per weight of turning codes into operands decides.  The
-// matrices are stored in the order in which mma.sync reads its operand (include/moe.h): a lane's
-// 16 bytes are four A fragments of m16n8k16, every 32-bit word one of them, and masks alone make
-// operands of it.  A code in the low bits of a 16-bit float, all else zero, is a subnormal number:
-// code * 2^-133 in bf16 (2^-24 in fp16), and 16 times that where the code lies four bits higher
-// (the step from the subnormal to the first normal numbers is even, so bf16's seven bits of
-// mantissa suffice).  w & 0x000f000f is the fragment's rows g, w & 0x00f000f0 its rows g + 8, and
-// w >> 8 has the other columns of both: five instructions for eight weights.  The 8 that every
-// code is too large by is -8 sum(x) over a group of columns, the same for all weights: it is made
-// once, where the rows arrive, and is what the group's sums start from.  The powers of two go
-// into the result at the end.  To keep bf16 products out of fp32's own subnormal range, the rows
-// are multiplied by 2^64 as they arrive in shared memory; so a row's numbers count as infinite
-// from 2^63 on.
-// The products with bf16 rows are exact in the fp32 accumulators; a group's sum is multiplied by
-// its scale in fp32.  8-bit rows (e4m3 with scales) are widened to fp16, also exactly, and their
-// scales join the weights' scales on the sums.  Nothing is rounded below 32 bits before the
-// output.
+// weights, per clock, so the instructions that turn codes into operands decide.  The matrices are
+// stored in the order in which mma.sync reads its operand (include/moe.h): a lane's 16 bytes are
+// four A fragments of m16n8k16, every 32-bit word one of them, and masks alone make operands of
+// it.  Bits in the low byte of a 16-bit float, all else zero, are the number bits * 2^-133 in bf16
+// (subnormal up to 127, and on evenly from there: the mantissa has seven bits), bits * 2^-24 in
+// fp16.  A byte holds the codes of rows g and g + 8; so w & 0x00ff00ff gives code(g) + 16
+// code(g + 8), w & 0x000f000f code(g) alone, and one byte permutation and one mask the same for
+// the word's other columns: four instructions for eight weights.  The fragment's rows g take the
+// first, its rows g + 8 the second, and the difference of their sums is 16 times the sum of row
+// g + 8.  The 8 that every code is too large by is -8 sum(x) over a group of columns, the same for
+// all weights: it is made once, where the rows arrive, and is what the group's sums start from.
+// The powers of two go into the result at the end.  To keep bf16 products out of fp32's own
+// subnormal range, the rows are multiplied by 2^64 as they arrive in shared memory; so a row's
+// numbers count as infinite from 2^63 on.  8-bit rows (e4m3 with scales) become fp16 there, and
+// their scales join the weights' scales on the sums.  All products are exact in the fp32
+// accumulators; a group's sum is multiplied by its scale in fp32, and nothing is rounded below 32
+// bits before the output.  (For one token at 4096 x 14336 x 2: 33 us with a subtraction for each
+// operand, 17.3 us with five instructions for a word, 16.2 us with four.  The fifth-generation
+// tensor cores would want the operands in shared memory first, at 16 bits a weight more than an
+// SM's shared memory moves at this rate; at these few rows mma.sync is 20 to 30 % busy.)
 //
-// A block of warps owns one tile of a group's rows (up to 32) and 32 output rows for every warp,
-// two blocks of 16 (for SwiGLU a gate block and its up block).  Every warp
+// A block of 16 warps, one on an SM, owns one tile of a group's rows (8 or 16) and 512 output
+// rows, each warp two blocks of 16 of them (for SwiGLU a gate block and its up block).  Every warp
 // runs a ring of its own in shared memory for the weights that it alone needs: each lane copies
-// asynchronously what that lane will read, kDepth steps of 256 columns ahead and on across
-// items, without a barrier.  The activation rows, which all warps need, come in chunks of
-// several steps into three buffers: every warp copies its part of a chunk two chunks ahead and
-// makes operands of it one chunk ahead, and mbarriers tell when all have, so the warps may run
-// apart by most of a chunk.  The items are dealt to the resident blocks in whole rounds; those
-// that are left, or all where there are few, are cut into 2, 4, 8 or 16
-// units, whichever ends first, whose warps share out the columns of fewer output rows.  Their
-// partial sums meet in shared memory and are added in order.
+// asynchronously what that lane will read, kDepth steps of 256 columns ahead and on across items,
+// without a barrier (registers held no more than two steps of 128, and waited for one another).
+// The activation rows, which all warps need, come in chunks of several steps into three buffers:
+// every warp copies its part of a chunk two chunks ahead and makes operands of it one chunk ahead,
+// and mbarriers tell when all have, so the warps may run apart by most of a chunk.
+//
+// The items are dealt to the resident blocks in whole rounds; those that are left, or all where
+// there are few, are cut into 2, 4, 8 or 16 units, whose warps share out the columns of fewer
+// output rows; their partial sums meet in shared memory and are added in order.  Where items are
+// few and their rows take the room that a cut needs, clusters of 2, 4 or 8 blocks share out the
+// columns instead, and the first adds the others' sums in order (33 8-bit rows of 14336 columns:
+// 204 us without, 61 us with them).
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
 #include <algorithm>
 #include <climits>
@@ -53,7 +59,6 @@ namespace moe {
 namespace {
 
 namespace cg = cooperative_groups;
-
 
 struct Args {
   const uint4* q;
@@ -222,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
   constexpr int kSteps = 256 / kGroup;  // groups in a step
   constexpr int kEl = kX8 ? 1 : 2;      // bytes of an input element
   __shared__ int32_t s_warp[kWarps];
-  __shared__ int32_t s_x_steps[kTile + 1];     // steps of a chunk of so many rows
+  __shared__ int32_t s_x_steps[kTile + 1];  // steps of a chunk of so many rows
   extern __shared__ __align__(1024) char s_ring[];  // the rings, the rows' buffers, partial sums
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -234,8 +239,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
   __shared__ int s_abort;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBuffers; ++i) {
-      tc::mbar_init(&s_full[i], kWarps);
-      tc::mbar_init(&s_free[i], kWarps);
+      mbar::init(&s_full[i], kWarps);
+      mbar::init(&s_free[i], kWarps);
     }
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -369,7 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
   const float* c_xs = nullptr;
   int n_copied = 0;        // chunks
   // of the two chunks copied last: rows, slots of a row, and those before the last column
-  int d_rows[2] = {0, 0}, d_over[2] = {1, 1}, d_steps[2] = {0, 0}, d_slots[2] = {0, 0}, d_inside[2] = {0, 0};
+  int d_rows[2] = {0, 0}, d_over[2] = {1, 1}, d_steps[2] = {0, 0};
+  int d_slots[2] = {0, 0}, d_inside[2] = {0, 0};
   bool dead = false;  // a wait ran out: nothing is stored any more
   auto copy_chunk = [&]() {
     if (c_it >= units) return;
@@ -390,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
     const int inside = min(slots, (a.cols - 256 * (k0 + st0)) >> 3);
     // every warp is done with what the buffer held
     if (n_copied >= kBuffers && !dead)
-      dead = !tc::mbar_wait(&s_free[c_buf], c_phase, &s_abort, a.status);
+      dead = !__all_sync(0xffffffffu, mbar::wait(&s_free[c_buf], c_phase, &s_abort, a.status));
     const int r = warp & (c_over - 1);
     if (r < c_rows) {
       const uint32_t to = x0 + c_buf * a.buf_bytes, at = to + r * pitch + 16 * lane;
@@ -445,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
       }
     }
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive(&s_full[m_buf]);
+    if (lane == 0) mbar::arrive(&s_full[m_buf]);
     m_buf = m_buf + 1 == kBuffers ? 0 : m_buf + 1;
     ++n_made;
   };
@@ -546,7 +552,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
       for (int n = 0; n < kN; ++n)
         x_off[n] = min(8 * n + g, im.tile_rows - 1) * x_pitch(im.x_steps) + 16 * t;
       for (int c0 = 0; c0 < im.steps; c0 += chunk) {
-        if (!dead) dead = !tc::mbar_wait(&s_full[buf], x_phase, &s_abort, a.status);
+        if (!dead)
+          dead = !__all_sync(0xffffffffu, mbar::wait(&s_full[buf], x_phase, &s_abort, a.status));
         const int n_now = dead ? 0 : n_mine, end = min(c0 + chunk, im.steps);
         const char* px = s_x + buf * a.buf_bytes + ks * 512;
         const char* po = s_x + buf * a.buf_bytes + sums_of(im.tile_rows, im.x_steps) +
@@ -558,86 +565,86 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
         int s = c0;
         bool copied = false;
         for (int stop = c0 + 1;; stop = end) {
-        for (; s < stop; ++s) {
-          copies_wait<kDepth - 1>();
-          __syncwarp();  // other lanes' scales
-          if (s < n_now) {
-            const char* pq = s_mine + at + lane * 16;
-            const uint32_t* ps = reinterpret_cast<const uint32_t*>(s_mine + at + kStepQ) + g;
-            // of the step's groups, the last there is
-            const int st = k0 + (s << im.log2) + ks, g_last = a.ng - 1 - st * kSteps;
-            float part[2][kN][4];
-            uint4 w[2];
+          for (; s < stop; ++s) {
+            copies_wait<kDepth - 1>();
+            __syncwarp();  // other lanes' scales
+            if (s < n_now) {
+              const char* pq = s_mine + at + lane * 16;
+              const uint32_t* ps = reinterpret_cast<const uint32_t*>(s_mine + at + kStepQ) + g;
+              // of the step's groups, the last there is
+              const int st = k0 + (s << im.log2) + ks, g_last = a.ng - 1 - st * kSteps;
+              float part[2][kN][4];
+              uint4 w[2];
 #pragma unroll
-            for (int h = 0; h < 8; ++h) {  // 32 columns each
-              if (h == 4 && 256 * st + 128 >= a.cols) break;
-              if (h % 2 == 0) {
-                w[0] = *reinterpret_cast<const uint4*>(pq + 256 * h);
-                w[1] = *reinterpret_cast<const uint4*>(pq + 256 * h + 2048);
-              }
-              uint4 b[kN];
-#pragma unroll
-              for (int n = 0; n < kN; ++n)
-                b[n] = *reinterpret_cast<const uint4*>(px + x_off[n] + 64 * h);
-              float off[kN][4];  // what a group's sums start from
-              if (h % (kGroup / 32) == 0) {
-#pragma unroll
-                for (int n = 0; n < kN; ++n) {
-                  const float2 o = *reinterpret_cast<const float2*>(
-                      po + (h / (kGroup / 32) * kTile + 8 * n) * 4);
-                  off[n][0] = 17.f * o.x;
-                  off[n][1] = 17.f * o.y;
-                  off[n][2] = o.x;
-                  off[n][3] = o.y;
+              for (int h = 0; h < 8; ++h) {  // 32 columns each
+                if (h == 4 && 256 * st + 128 >= a.cols) break;
+                if (h % 2 == 0) {
+                  w[0] = *reinterpret_cast<const uint4*>(pq + 256 * h);
+                  w[1] = *reinterpret_cast<const uint4*>(pq + 256 * h + 2048);
                 }
-              }
+                uint4 b[kN];
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
+                for (int n = 0; n < kN; ++n)
+                  b[n] = *reinterpret_cast<const uint4*>(px + x_off[n] + 64 * h);
+                float off[kN][4];  // what a group's sums start from
+                if (h % (kGroup / 32) == 0) {
+#pragma unroll
+                  for (int n = 0; n < kN; ++n) {
+                    const float2 o = *reinterpret_cast<const float2*>(
+                        po + (h / (kGroup / 32) * kTile + 8 * n) * 4);
+                    off[n][0] = 17.f * o.x;
+                    off[n][1] = 17.f * o.y;
+                    off[n][2] = o.x;
+                    off[n][3] = o.y;
+                  }
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                  for (int m = 0; m < 2; ++m) {
+                    const uint32_t word = (h & 1) ? (j ? w[m].w : w[m].z) : (j ? w[m].y : w[m].x);
+                    uint32_t fa[4];
+                    widen(word, fa);
+#pragma unroll
+                    for (int n = 0; n < kN; ++n)
+                      mma<kX8>(part[m][n], fa, j ? b[n].z : b[n].x, j ? b[n].w : b[n].y,
+                               j == 0 && h % (kGroup / 32) == 0 ? off[n] : part[m][n]);
+                  }
+                }
+                if ((h + 1) % (kGroup / 32) != 0) continue;
+                const int gi = kGroup == 128 ? h / 4 : min(h / (kGroup / 32), g_last);
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
-                  const uint32_t word = (h & 1) ? (j ? w[m].w : w[m].z) : (j ? w[m].y : w[m].x);
-                  uint32_t fa[4];
-                  widen(word, fa);
+                  const uint32_t sw = ps[(m * kSteps + gi) * 8];
+                  const float lo = __uint_as_float(sw << 16), up = __uint_as_float(sw & 0xffff0000u);
 #pragma unroll
-                  for (int n = 0; n < kN; ++n)
-                    mma<kX8>(part[m][n], fa, j ? b[n].z : b[n].x, j ? b[n].w : b[n].y,
-                             j == 0 && h % (kGroup / 32) == 0 ? off[n] : part[m][n]);
-                }
-              }
-              if ((h + 1) % (kGroup / 32) != 0) continue;
-              const int gi = kGroup == 128 ? h / 4 : min(h / (kGroup / 32), g_last);
-#pragma unroll
-              for (int m = 0; m < 2; ++m) {
-                const uint32_t sw = ps[(m * kSteps + gi) * 8];
-                const float lo = __uint_as_float(sw << 16), up = __uint_as_float(sw & 0xffff0000u);
-#pragma unroll
-                for (int n = 0; n < kN; ++n) {
-                  // rows g, then rows g + 8 (16 times as large)
-                  const float s0 = part[m][n][2], s1 = part[m][n][3];
-                  const float s2 = part[m][n][0] - s0, s3 = part[m][n][1] - s1;
-                  if (kX8) {
-                    const float2 xs = *reinterpret_cast<const float2*>(pxs + (h / 4 * kTile + 8 * n) * 4);
-                    acc[m][n][0] = fmaf(s0, lo * xs.x, acc[m][n][0]);
-                    acc[m][n][1] = fmaf(s1, lo * xs.y, acc[m][n][1]);
-                    acc[m][n][2] = fmaf(s2, up * xs.x, acc[m][n][2]);
-                    acc[m][n][3] = fmaf(s3, up * xs.y, acc[m][n][3]);
-                  } else {
-                    acc[m][n][0] = fmaf(s0, lo, acc[m][n][0]);
-                    acc[m][n][1] = fmaf(s1, lo, acc[m][n][1]);
-                    acc[m][n][2] = fmaf(s2, up, acc[m][n][2]);
-                    acc[m][n][3] = fmaf(s3, up, acc[m][n][3]);
+                  for (int n = 0; n < kN; ++n) {
+                    // rows g, then rows g + 8 (16 times as large)
+                    const float s0 = part[m][n][2], s1 = part[m][n][3];
+                    const float s2 = part[m][n][0] - s0, s3 = part[m][n][1] - s1;
+                    if (kX8) {
+                      const float2 xs = *reinterpret_cast<const float2*>(pxs + (h / 4 * kTile + 8 * n) * 4);
+                      acc[m][n][0] = fmaf(s0, lo * xs.x, acc[m][n][0]);
+                      acc[m][n][1] = fmaf(s1, lo * xs.y, acc[m][n][1]);
+                      acc[m][n][2] = fmaf(s2, up * xs.x, acc[m][n][2]);
+                      acc[m][n][3] = fmaf(s3, up * xs.y, acc[m][n][3]);
+                    } else {
+                      acc[m][n][0] = fmaf(s0, lo, acc[m][n][0]);
+                      acc[m][n][1] = fmaf(s1, lo, acc[m][n][1]);
+                      acc[m][n][2] = fmaf(s2, up, acc[m][n][2]);
+                      acc[m][n][3] = fmaf(s3, up, acc[m][n][3]);
+                    }
                   }
                 }
               }
             }
+            px += 512 << im.log2;
+            po += kSteps * kTile * 4 << im.log2;
+            if (kX8) pxs += 2 * kTile * 4 << im.log2;
+            __syncwarp();  // the slot's scales have been read
+            fetch(at);
+            at = at + kStep == kDepth * kStep ? 0 : at + kStep;
           }
-          px += 512 << im.log2;
-          po += kSteps * kTile * 4 << im.log2;
-          if (kX8) pxs += 2 * kTile * 4 << im.log2;
-          __syncwarp();  // the slot's scales have been read
-          fetch(at);
-          at = at + kStep == kDepth * kStep ? 0 : at + kStep;
-        }
           if (copied) break;
           copied = true;
           if (end - c0 < kDepth) {
@@ -647,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
           copy_chunk();
         }
         if (end - c0 >= kDepth) make_chunk();  // the next chunk landed a chunk ago
-        if (lane == 0) tc::mbar_arrive(&s_free[buf]);
+        if (lane == 0) mbar::arrive(&s_free[buf]);
         if (++buf == kBuffers) {
           buf = 0;
           x_phase ^= 1;
