@@ -350,7 +350,7 @@ MOE_API moe_status moe_w4_quantize(const moe_w4* w, const void* W, moe_stream_t 
  * values of 2^63 and more count as infinite, and a NaN or infinity makes its row's outputs NaN.
  *   x        bf16 [x_rows][cols], or with x_scale e4m3 [x_rows][cols]: x_scale fp32
  *            [x_rows][ceil(cols / 128)] (x_group = 128) or [x_rows][1] (x_group = 0), the two
- *            8-bit outputs of moe_rms_norm
+ *            8-bit outputs of moe_rms_norm; x_rows at least 1 where there are rows of out
  *   offsets  [mats + 1] device int32: group e is rows [offsets[e], offsets[e+1]) of out, through
  *            matrix e; NULL (mats = 1 only): all rows are one group
  *   row_index [rows] device int32 or NULL: out row r reads x row row_index[r] (NULL: r)

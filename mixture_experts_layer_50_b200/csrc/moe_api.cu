@@ -1299,6 +1299,8 @@ moe_status moe_w4_matmul(const moe_w4* w, const void* x, const float* x_scale, i
     return fail(MOE_ERR_INVALID_ARG, "x_group must be 0 or 128");
   if (row_index == nullptr && x_rows < rows)
     return fail(MOE_ERR_INVALID_ARG, "x has fewer rows than out");
+  if (x_rows == 0 && rows > 0)  // (a row index out of range reads row 0 and drops it)
+    return fail(MOE_ERR_INVALID_ARG, "x has no rows");
   if (!(clamp == clamp)) return fail(MOE_ERR_INVALID_ARG, "clamp is NaN");
   if (out_dtype != MOE_DT_BF16 && out_dtype != MOE_DT_F32)
     return fail(MOE_ERR_INVALID_ARG, "unknown out_dtype");

@@ -920,7 +920,7 @@ cudaError_t launch_w4(const W4Gemm& p, cudaStream_t stream, int* launches) {
   a.out = p.out;
   a.out_f32 = p.out_f32;
   a.status = p.status;
-  // rows of a tile: enough for the largest group there can be, 32 at most
+  // rows of a tile: enough for the largest group there can be, 16 at most
   const int64_t most = p.has_shared ? (p.shared_rows > p.max_group_rows ? p.shared_rows : p.max_group_rows)
                                     : p.max_group_rows;
   const int nt = most <= 8 ? 1 : 2;

@@ -81,6 +81,13 @@ def test_w4_matmul_needs_offsets_for_several_matrices():
     assert lib.moe_w4_matmul(ctypes.byref(w), FAKE, None, 128, 8, None, None, 8, 0.0, FAKE, 0, None, None) == 1
 
 
+def test_w4_matmul_needs_a_row_to_read():
+    call = lambda rows: lib.moe_w4_matmul(ctypes.byref(w4()), FAKE, None, 128, 0, None, FAKE, rows, 0.0, FAKE, 0, None,
+                                          None)
+    assert call(8) == 1 and b"no rows" in lib.moe_last_error()
+    assert call(0) == 0
+
+
 GU = dict(mats=4, parts=2, rows=64, cols=128)
 DOWN = dict(mats=4, parts=1, rows=128, cols=64)
 
