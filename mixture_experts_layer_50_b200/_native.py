@@ -435,6 +435,13 @@ class W4Matrix:
         return w
 
 
+def _w4(w: W4Matrix):
+    """The C form of a matrix of the current device."""
+    if w.q.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"the 4-bit matrix is on cuda:{w.q.get_device()}, not on the current device")
+    return ctypes.byref(w.c)
+
+
 def _row_scale(x, x_scale, group):
     """Checks 8-bit (with x_scale) or bf16 rows; returns both pointers."""
     n, d = x.shape
@@ -453,7 +460,7 @@ def moe_w4_matmul(w: W4Matrix, *, x, x_scale=None, x_group=128, offsets=None, ro
     R = out.shape[0]
     px, ps = _row_scale(x, x_scale, x_group)
     st = lib.moe_w4_matmul(
-        ctypes.byref(w.c), px, ps, x_group, n, _typed(offsets, "offsets", torch.int32, w.mats + 1),
+        _w4(w), px, ps, x_group, n, _typed(offsets, "offsets", torch.int32, w.mats + 1),
         _typed(row_index, "row_index", torch.int32, R), R, clamp,
         _typed(out, "out", (torch.bfloat16, torch.float32), R, w.rows),
         F32 if out.dtype == torch.float32 else BF16, _ptr(ws), _stream(stream))
@@ -469,8 +476,8 @@ def moe_expert_ffn_w4(cfg, *, x, x_scale=None, offsets, row_token, W_gu: W4Matri
     nk = cfg.N * cfg.k
     st = lib.moe_expert_ffn_w4(
         ctypes.byref(cfg), px, ps, _typed(offsets, "offsets", torch.int32, cfg.E + 1),
-        _typed(row_token, "row_token", torch.int32, nk), ctypes.byref(W_gu.c),
-        ctypes.byref(W_down.c),
+        _typed(row_token, "row_token", torch.int32, nk), _w4(W_gu),
+        _w4(W_down),
         _typed(ye, "ye", torch.bfloat16, nk + cfg.n_shared * cfg.N, cfg.d), _ptr(ws),
         _stream(stream))
     _check(st, "moe_expert_ffn_w4")
@@ -488,7 +495,7 @@ def moe_forward_w4(cfg, *, x, x8=None, x8_scale=None, W_g, W_gu: W4Matrix, W_dow
         ctypes.byref(cfg), _typed(x, "x", torch.bfloat16, N, d), _typed(x8, "x8", _E4M3, N, d),
         _typed(x8_scale, "x8_scale", torch.float32, N, (d + 127) // 128),
         _typed(W_g, "W_g", torch.bfloat16, cfg.E, d), _ptr(logit_offset), _ptr(bias),
-        _ptr(modality), ctypes.byref(W_gu.c), ctypes.byref(W_down.c),
+        _ptr(modality), _w4(W_gu), _w4(W_down),
         _typed(y, "y", torch.bfloat16, N, d), ctypes.byref(ro) if ro is not None else None,
         _ptr(ws), _stream(stream))
     _check(st, "moe_forward_w4")

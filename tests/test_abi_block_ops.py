@@ -142,3 +142,31 @@ def test_binding_checks_types_and_shapes():
         nat.W4Matrix.quantize(torch.zeros(1, 33, 64, dtype=torch.bfloat16), parts=2)
     with pytest.raises(nat.MoeError):
         nat.W4Matrix(torch.zeros(1, 1, 1, 1, 512, dtype=torch.uint8), torch.zeros(1), rows=16, cols=60, group=64)
+
+
+class ElsewhereMatrix:
+    """Stands for a W4Matrix on a device that is not the current one."""
+    class q:
+        get_device = staticmethod(lambda: 7)
+    mats, parts, rows, cols, group = 4, 1, 64, 128, 64
+    c = w4()
+
+
+class Uncalled:
+    def __getattr__(self, name):
+        return lambda *a: pytest.fail(f"{name} was called")
+
+
+def test_4_bit_matrices_of_another_device_are_refused(monkeypatch):
+    monkeypatch.setattr(nat.torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(nat, "_typed", lambda t, *a: 0)
+    monkeypatch.setattr(nat, "_stream", lambda s: None)
+    monkeypatch.setattr(nat, "_ptr", lambda t: 0)
+    monkeypatch.setattr(nat, "lib", Uncalled())
+    m, x = ElsewhereMatrix(), torch.zeros(16, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="cuda:7"):
+        nat.moe_w4_matmul(m, x=x, out=torch.zeros(16, 64))
+    with pytest.raises(ValueError, match="cuda:7"):
+        nat.moe_expert_ffn_w4(cfg(), x=x, offsets=None, row_token=None, W_gu=m, W_down=m, ye=None, ws=None)
+    with pytest.raises(ValueError, match="cuda:7"):
+        nat.moe_forward_w4(cfg(), x=x, W_g=None, W_gu=m, W_down=m, y=x, ws=None)
