@@ -1,6 +1,7 @@
 """MoELayer: a layer's device weights and workspace behind one ``forward`` call."""
 from __future__ import annotations
 
+import contextlib
 from typing import Optional
 
 import torch
@@ -139,6 +140,14 @@ class MoELayer:
         return nat.moe_check_status(self.ws, stream)
 
 
+def _on(stream):
+    """Memory taken inside belongs to ``stream``: what the current stream still does with memory
+    that it has given back does not meet what ``stream`` writes."""
+    if isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)
+    return contextlib.nullcontext()
+
+
 class W4MoELayer(MoELayer):
     """A bf16 layer whose expert weights are held in 4 bits (``moe_forward_w4``), for decode.
 
@@ -183,7 +192,8 @@ class W4MoELayer(MoELayer):
         N = x.shape[0]
         self._check_tokens(N)
         if y is None:
-            y = torch.empty_like(x)
+            with _on(stream):
+                y = torch.empty_like(x)
         nat.moe_forward_w4(self.config(N), x=x, x8=x8, x8_scale=x8_scale, W_g=self.W_g,
                            W_gu=self.W_gu, W_down=self.W_down, y=y,
                            logit_offset=self.logit_offset, bias=self.bias, modality=modality,
@@ -195,15 +205,16 @@ class W4MoELayer(MoELayer):
                        stream=None):
         """The layer of RMS norm(x + residual) * weight; returns (y, x + residual)."""
         N, d = x.shape
-        h, total = torch.empty_like(x), torch.empty_like(x)
-        h8 = torch.empty((N, d), dtype=torch.float8_e4m3fn, device=x.device)
-        h8_scale = torch.empty((N, (d + 127) // 128), device=x.device)
+        with _on(stream):
+            h, total = torch.empty_like(x), torch.empty_like(x)
+            h8 = torch.empty((N, d), dtype=torch.float8_e4m3fn, device=x.device)
+            h8_scale = torch.empty((N, (d + 127) // 128), device=x.device)
         nat.moe_rms_norm(x=x, residual=residual, weight=weight, eps=eps, y=h, residual_out=total,
                          y8=h8, y8_scale=h8_scale, stream=stream)
         y = self.forward(h, modality=modality, route_out=route_out, stream=stream, x8=h8,
                          x8_scale=h8_scale)
         if isinstance(stream, torch.cuda.Stream):
-            for t in (x, residual, h, total, h8, h8_scale, y):
+            for t in (x, residual):
                 t.record_stream(stream)
         return y, total
 

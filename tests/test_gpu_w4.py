@@ -533,3 +533,23 @@ def test_two_graphs_share_a_workspace():
     torch.cuda.synchronize()
     for _, got, want, _ in graphs:
         assert torch.equal(got, want)
+
+
+def test_layer_on_another_stream_takes_its_own_memory():
+    shape = W.PRESETS["dsv3-n64"].replace(N=20, d=256, E=8, k=2, F=128)
+    t = W.make_inputs(shape, device="cuda")
+    from mixture_experts_layer_50_b200 import MoELayer, W4MoELayer
+    w4 = W4MoELayer.from_layer(MoELayer.from_workload(shape, t))
+    want, total = w4.forward_normed(t["x"], t["x"])
+    plain = w4.forward(t["x"])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    # memory that the current stream has given back, and may still be writing
+    freed = [torch.empty_like(want) for _ in range(6)]
+    places = {f.data_ptr() for f in freed}
+    del freed
+    got, got_total = w4.forward_normed(t["x"], t["x"], stream=side)
+    got_plain = w4.forward(t["x"], stream=side)
+    torch.cuda.synchronize()
+    assert not places & {g.data_ptr() for g in (got, got_total, got_plain)}
+    assert torch.equal(got, want) and torch.equal(got_total, total) and torch.equal(got_plain, plain)
