@@ -18,7 +18,13 @@
 // additions; the last block to finish turns the sums into P and the loss.  (Additions to shared
 // memory bound the count: one cluster took 15 us for 16384 tokens of six experts.)
 //
-// Bound: one read of the logits and one write of the gradient.
+// Bound: one read of the logits and one write of the gradient; small batches by the two launches
+// (64 tokens of 256 experts and 8191 of 8 take 8 us each in a captured graph).  For 16384 padded
+// tokens of 384 experts the reads and writes are 7.8 us of 21.5: the count takes 5 us, its
+// additions and its cluster's meeting; in the row pass a warp issues in 42 % of its slots with 36 %
+// of an SM's threads (79 registers hold twelve experts a lane, the next token's logits and the
+// sums of P), and waits for two or three reductions over the warp per token.  Reading a token ahead
+// and 16 bytes at a time (every fourth lane's experts apart) took the whole from 37.6 us.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
