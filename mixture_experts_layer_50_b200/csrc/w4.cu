@@ -36,12 +36,14 @@
 // every warp copies its part of a chunk two chunks ahead and makes operands of it one chunk ahead,
 // and mbarriers tell when all have, so the warps may run apart by most of a chunk.
 //
-// The items are dealt to the resident blocks in whole rounds; those that are left, or all where
-// there are few, are cut into 2, 4, 8 or 16 units, whose warps share out the columns of fewer
-// output rows; their partial sums meet in shared memory and are added in order.  Where items are
-// few and their rows take the room that a cut needs, clusters of 2, 4 or 8 blocks share out the
-// columns instead, and the first adds the others' sums in order (33 8-bit rows of 14336 columns:
-// 204 us without, 61 us with them).
+// The items are dealt to the resident blocks in whole rounds, there and back, those of more than 8
+// rows first: they take nearly twice as long as the others, and so meet the cheapest at the end (37
+// tokens on 48 experts and a shared one: 224 us, 269 us in the groups' order).  Those that are
+// left, or all where there are few, are cut into 2, 4, 8 or 16 units, whose warps share out the
+// columns of fewer output rows; their partial sums meet in shared memory and are added in order.
+// Where items are few and their rows take the room that a cut needs, clusters of 2 to 8 blocks share
+// out the columns instead, and the first adds the others' sums in order (33 8-bit rows of 14336
+// columns: 204 us without, 61 us in clusters of 4, 55 us of 6).
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
@@ -226,15 +228,19 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
   constexpr int kTile = 8 * kNt;        // rows of a group that one item takes
   constexpr int kSteps = 256 / kGroup;  // groups in a step
   constexpr int kEl = kX8 ? 1 : 2;      // bytes of an input element
-  __shared__ int32_t s_warp[kWarps];
+  using Count = std::conditional_t<kNt == 1, int, int64_t>;  // tiles; light ones in the upper half
+  __shared__ Count s_warp[kWarps];
   __shared__ int32_t s_x_steps[kTile + 1];  // steps of a chunk of so many rows
   extern __shared__ __align__(1024) char s_ring[];  // the rings, the rows' buffers, partial sums
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int n_all = a.n_groups + a.has_shared;
-  int32_t* const s_first = reinterpret_cast<int32_t*>(s_ring + a.tables);  // first tiles of groups
-  int32_t* const s_row = s_first + n_all + 1;                              // their first rows
-  int32_t* const s_rows = s_row + n_all;                                   // and their rows
+  // the groups' first tiles of more than 8 rows (kNt = 1: all tiles), their first tiles of at most
+  // 8, which come behind all others, their first rows, and their rows
+  int32_t* const s_first = reinterpret_cast<int32_t*>(s_ring + a.tables);
+  int32_t* const s_light = s_first + n_all + 1;
+  int32_t* const s_row = s_light + n_all + 1;
+  int32_t* const s_rows = s_row + n_all;
   __shared__ uint64_t s_full[kBuffers], s_free[kBuffers];
   __shared__ int s_abort;
   if (threadIdx.x == 0) {
@@ -270,36 +276,45 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
     // tiles of every group, and their exclusive scan
     const int per = (n_all + kThreads - 1) / kThreads;
     const int e0 = threadIdx.x * per;
-    int mine = 0;
+    Count mine = 0;
     bool bad = false;
     for (int e = e0; e < e0 + per && e < n_all; ++e) {
       int first, n = group_rows(e, first);
       if (n < 0) bad = true, n = 0;
       const int tiles = (n + kTile - 1) / kTile;
-      s_first[e] = tiles;
+      const bool light = kNt > 1 && n % kTile != 0 && n % kTile <= 8;
+      s_first[e] = tiles - light;
+      s_light[e] = light;
       s_row[e] = first;
       s_rows[e] = n;
-      mine += tiles;
+      mine += tiles - light;
+      if constexpr (kNt > 1) mine += (int64_t)light << 32;
     }
     if (bad && blockIdx.x == 0) report_status(a.status, kStatusInvalidInput);
     if (threadIdx.x >= 1 && threadIdx.x <= kTile)
       s_x_steps[threadIdx.x] = x_steps_of(a.buf_bytes, kX8, kTile, threadIdx.x, kGroup);
-    int incl = mine;
+    Count incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      const Count v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
     if (lane == 31) s_warp[warp] = incl;
     __syncthreads();
-    int at = incl - mine;
-    for (int w = 0; w < warp; ++w) at += s_warp[w];
+    Count sum = incl - mine;
+    for (int w = 0; w < warp; ++w) sum += s_warp[w];
+    int at = (int)sum, at_light = kNt > 1 ? (int)((int64_t)sum >> 32) : 0;
     for (int e = e0; e < e0 + per && e < n_all; ++e) {
-      const int tiles = s_first[e];
+      const int tiles = s_first[e], light = s_light[e];
       s_first[e] = at;
+      s_light[e] = at_light;
       at += tiles;
+      at_light += light;
     }
-    if (threadIdx.x == kThreads - 1) s_first[n_all] = at;
+    if (threadIdx.x == kThreads - 1) {
+      s_first[n_all] = at;
+      s_light[n_all] = at_light;
+    }
     bad_index = __syncthreads_or(bad_index);
   }
   // The blocks of a cluster work on the same items, each on its run of the steps, k0 onwards.
@@ -310,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
   // blocks are cut into 2^cut units
   const int chunks = (a.pairs + kWarps - 1) / kWarps;
   const int n_blocks = (int)gridDim.x / per, block = (int)blockIdx.x / per;
-  const int items = s_first[n_all] * chunks;  // (units are below 2^31: checked on the host)
+  const int n_full = s_first[n_all], items = (n_full + s_light[n_all]) * chunks;  // (units are below 2^31: checked on the host)
   const int rest = items % n_blocks, whole = items - rest;
   int cut = 0;
   for (int c = 1; 1 << c <= a.max_split; ++c) {
@@ -320,6 +335,13 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
   }
   const int units = whole + (rest << cut);
 
+  // A block's units, one in each round: its place there and back, so that what the costlier tiles
+  // at the front take longer is made up for by cheaper ones.  `step` is from one to the next.
+  const int first_step = 2 * (n_blocks - block) - 1;
+  auto next_unit = [&](int& unit, int& step) {
+    unit += step;
+    step = 2 * n_blocks - step;
+  };
   auto item_at = [&](int unit) {
     Item r;
     int it = unit, part = 0;
@@ -329,20 +351,24 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
       r.log2 = cut;
       r.split = 1 << cut;
     }
-    const int tile = (int)((unsigned)it / (unsigned)chunks);
+    int tile = (int)((unsigned)it / (unsigned)chunks);
     r.pair0 = (it - tile * chunks) * kWarps + part * (kWarps >> r.log2);
     r.n_pairs = min(kWarps >> r.log2, a.pairs - r.pair0);
     r.steps = (n_steps + r.split - 1) >> r.log2;
-    int hi = n_all;  // the group that owns the tile: s_first[e] <= tile < s_first[e + 1]
+    const bool light = kNt > 1 && tile >= n_full;
+    const int32_t* const table = light ? s_light : s_first;
+    if (light) tile -= n_full;
+    int hi = n_all;  // the group that owns the tile: table[e] <= tile < table[e + 1]
     while (hi - r.e > 1) {
       const int mid = (r.e + hi) >> 1;
-      if (s_first[mid] <= tile)
+      if (table[mid] <= tile)
         r.e = mid;
       else
         hi = mid;
     }
     r.shared = r.e >= a.n_groups;
-    const int first = s_row[r.e], row0 = (tile - s_first[r.e]) * kTile;
+    const int first = s_row[r.e];
+    const int row0 = light ? s_rows[r.e] / kTile * kTile : (tile - table[r.e]) * kTile;
     r.tile_rows = min(kTile, s_rows[r.e] - row0);
     r.x_steps = min(s_x_steps[r.tile_rows], n_steps + r.split - 1) >> r.log2 << r.log2;
     r.out_row0 = (r.shared ? a.shared_out_row0 : first) + row0;
@@ -367,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
   auto scales_of = [](int rows, int x_steps) {
     return rows * x_pitch(x_steps) + x_steps * kSteps * kTile * 4;
   };
-  int c_it = block;  // unit and first step of the chunk to copy next
+  int c_it = block, c_go = first_step;  // unit and first step of the chunk to copy next
   int c_s = 0, c_steps = 0, c_log2 = 0, c_rows = 0, c_over = 1, c_x_steps = 0, c_buf = 0;
   uint32_t c_phase = 0;    // of the buffer's last freeing
   const char* c_x = nullptr;  // the warp's row at the next chunk's first column
@@ -420,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
     c_s += c_x_steps >> c_log2;
     if (c_s >= c_steps) {
       c_s = 0;
-      c_it += n_blocks;
+      next_unit(c_it, c_go);
     }
   };
   // Operands, and sums by groups, of the warp's part of a chunk that has landed: the chunk
@@ -459,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
   // ---- weights: the warp's ring; step f_s of the share of unit f_it is fetched next ----
   char* const s_mine = s_ring + warp * (kDepth * kStep);
   const uint32_t ring0 = (uint32_t)__cvta_generic_to_shared(s_mine) + lane * 16;
-  int f_it = block;
+  int f_it = block, f_go = first_step;
   int f_plain = 0;                       // steps of the share before its last one
   int f_s = 0, f_steps = 0, f_n = 0;     // then: the step, the unit's steps, and the share's
   int f_last = 0, f_dq = 0, f_ds = 0;    // the last step's place; bytes from a step to the next
@@ -514,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
         if (lane < 4 * kSteps && f_last * kSteps + s_c / 2 < a.ng) copy16(dst + kStepQ, fs);
       }
       if (++f_s >= f_steps) {
-        f_it += n_blocks;
+        next_unit(f_it, f_go);
         fetch_item();
       }
     }
@@ -531,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
   make_chunk();
   int buf = 0, at = 0;
   uint32_t x_phase = 0;
-  for (int unit = block; unit < units; unit += n_blocks) {
+  for (int unit = block, go = first_step; unit < units; next_unit(unit, go)) {
     const Item im = item_at(unit);
     const int ks = warp & (im.split - 1), pair = im.pair0 + (warp >> im.log2);
     const int n_mine = steps_of(im), chunk = im.x_steps >> im.log2;
@@ -930,24 +956,24 @@ cudaError_t launch_w4(const W4Gemm& p, cudaStream_t stream, int* launches) {
   const int rows = (int)(most < tile ? most : tile);  // the most of a tile
   // shared memory: the rings, the partial sums, and three buffers of input rows, in which a
   // chunk of a step for each share of a cut item has to fit
-  const int table_bytes = 4 * (3 * (p.n_groups + p.has_shared) + 1);
+  const int table_bytes = 4 * (4 * (p.n_groups + p.has_shared) + 2);
   const auto buffer = [&](int split, int cluster) {
     const int room = (kDynamicSmem - table_bytes - kWarps * kDepth * kStep -
                       sum_bytes(nt, split, cluster)) / kBuffers / 128 * 128;
     const int all = x_bytes(x8, tile, rows, n_steps < 16 ? n_steps : 16, p.group);
     return room < all ? room : all;
   };
-  // Clusters of 1, 2, 4 or 8 blocks (of 8, two to each of the device's eight clusters of SMs), and
-  // the finest cut that there is room for, whichever has the items that are expected done first;
-  // a unit's hand-over takes about a step.
+  // Clusters of 1 to 8 blocks, and the finest cut that there is room for, whichever has the items
+  // that are expected done first; a unit's hand-over takes about a step.  Clusters lie within the
+  // device's eight groups of SMs: of 148 SMs, 18 in each are counted on (all, for 1, 2 or 4).
   const int64_t shared_tiles = p.has_shared ? (p.shared_rows + tile - 1) / tile : 0;
   const int64_t reached = p.max_rows < p.n_groups ? p.max_rows : p.n_groups;
   const int64_t chunks = (a.pairs + kWarps - 1) / kWarps;
   const int64_t expected = ((p.offsets == nullptr ? (p.max_rows + tile - 1) / tile : reached) +
                             shared_tiles) * chunks;
-  const auto clusters_of = [&](int c) { return c == 8 && sms >= 144 ? 16 : sms / c; };
+  const auto clusters_of = [&](int c) { return c <= 2 || c == 4 ? sms / c : sms / 8 / c * 8; };
   int64_t least = -1;
-  for (int c = 1; c <= 8 && c <= n_steps && c <= sms; c *= 2) {
+  for (int c = 1; c <= 8 && c <= n_steps && (c == 1 || c <= sms / 8); ++c) {
     const int n = clusters_of(c), steps = (n_steps + c - 1) / c;
     int rest = INT32_MAX;
     for (int k = 0; 1 << k <= kWarps && 1 << k <= steps; ++k) {
