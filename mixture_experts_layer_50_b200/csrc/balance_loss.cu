@@ -65,6 +65,7 @@ __global__ void __cluster_dims__(kCountCtas, 1, 1) __launch_bounds__(kCountThrea
                          int64_t N, int E, int k, int32_t* __restrict__ counts, LossScratch out,
                          int* status) {
   pdl_wait();
+  pdl_release();  // the row pass may load logits: what made them has ended
   extern __shared__ int32_t s_count[];  // [E], then the block's tokens
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank();
@@ -164,32 +165,10 @@ __device__ __forceinline__ int expert_of(int ti, int j) {
 template <int kTeam, int kEpl, bool kVec, bool kSigmoid>
 __global__ void __launch_bounds__(kLossThreads) balance_loss_kernel(const LossArgs a) {
   constexpr int kTeams = kLossThreads / kTeam;
-  pdl_wait();
   extern __shared__ float s_f[];  // f [E]; then [kTeams][E] sums
   const int E = a.E;
   float* const s_p = s_f + E;
   const int ti = threadIdx.x % kTeam, team = threadIdx.x / kTeam;
-  int T = 0;
-  for (int c = 0; c < a.s.n; ++c) T += a.s.tokens[c];
-  const double per = 1.0 / ((double)(T > 0 ? T : 1) * a.k);
-  for (int e = threadIdx.x; e < E; e += kLossThreads) {
-    int n = 0;
-#pragma unroll 4
-    for (int c = 0; c < a.s.n; ++c) n += a.s.counts[c * E + e];
-    s_f[e] = (float)(n * per);
-    s_p[e] = (float)(n * per - 1.0 / E);
-    if (a.counts != nullptr && blockIdx.x == 0) a.counts[e] = n;
-  }
-  __syncthreads();
-  const float g = (a.grad_loss != nullptr ? *a.grad_loss : 1.f) * a.alpha * (float)E /
-                  (float)(T > 0 ? T : 1);
-  float f0[kEpl], acc[kEpl];
-#pragma unroll
-  for (int j = 0; j < kEpl; ++j) {
-    const int e = expert_of<kTeam, kVec>(ti, j);
-    f0[j] = e < E ? s_p[e] : 0.f;
-    acc[j] = 0.f;
-  }
   // a token's logits, -infinity where there are none
   auto load = [&](int64_t t, float (&z)[kEpl]) {
     const bool live = t < a.N && (a.mask == nullptr || a.mask[t] != 0);
@@ -210,10 +189,35 @@ __global__ void __launch_bounds__(kLossThreads) balance_loss_kernel(const LossAr
     }
     return live;
   };
-  // every team of the block takes the same number of steps: the shuffles need whole warps
-  const int64_t step = (int64_t)gridDim.x * kTeams;
+  // The first tokens' logits are on their way before the counts are there: the count kernel lets
+  // this one start after all that came before itself has ended.
   float next[kEpl];
   bool next_live = load((int64_t)blockIdx.x * kTeams + team, next);
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int T = __reduce_add_sync(0xffffffffu, lane < a.s.n ? a.s.tokens[lane] : 0);
+  const double per = 1.0 / ((double)(T > 0 ? T : 1) * a.k);
+  for (int e = threadIdx.x; e < E; e += kLossThreads) {
+    int n = 0;
+#pragma unroll
+    for (int c = 0; c < kMaxCounts; ++c)
+      if (c < a.s.n) n += a.s.counts[c * E + e];
+    s_f[e] = (float)(n * per);
+    s_p[e] = (float)(n * per - 1.0 / E);
+    if (a.counts != nullptr && blockIdx.x == 0) a.counts[e] = n;
+  }
+  __syncthreads();
+  const float g = (a.grad_loss != nullptr ? *a.grad_loss : 1.f) * a.alpha * (float)E /
+                  (float)(T > 0 ? T : 1);
+  float f0[kEpl], acc[kEpl];
+#pragma unroll
+  for (int j = 0; j < kEpl; ++j) {
+    const int e = expert_of<kTeam, kVec>(ti, j);
+    f0[j] = e < E ? s_p[e] : 0.f;
+    acc[j] = 0.f;
+  }
+  // every team of the block takes the same number of steps: the shuffles need whole warps
+  const int64_t step = (int64_t)gridDim.x * kTeams;
   for (int64_t t0 = (int64_t)blockIdx.x * kTeams; t0 < a.N; t0 += step) {
     const int64_t t = t0 + team;
     const bool live = next_live;
