@@ -19,12 +19,13 @@
 // memory bound the count: one cluster took 15 us for 16384 tokens of six experts.)
 //
 // Bound: one read of the logits and one write of the gradient; small batches by the two launches
-// (64 tokens of 256 experts and 8191 of 8 take 8 us each in a captured graph).  For 16384 padded
-// tokens of 384 experts the reads and writes are 7.8 us of 21.5: the count takes 5 us, its
-// additions and its cluster's meeting; in the row pass a warp issues in 42 % of its slots with 36 %
-// of an SM's threads (79 registers hold twelve experts a lane, the next token's logits and the
-// sums of P), and waits for two or three reductions over the warp per token.  Reading a token ahead
-// and 16 bytes at a time (every fourth lane's experts apart) took the whole from 37.6 us.
+// (64 tokens of 256 experts and 8191 of 8 take 7.3 us each in a captured graph).  For 16384 padded
+// tokens of 384 experts the reads and writes are 7.8 us of 19.0: the count takes 5 us, its
+// additions and its cluster's meeting; in the row pass a scheduler issues in 42 % of its slots with 36 %
+// of an SM's threads (80 registers hold twelve experts a lane, the next token's logits and the
+// sums of P), and warps wait for two or three reductions per token.  Reading a token ahead and 16
+// bytes at a time took the whole from 37.6 to 21.5 us; starting the row pass beside the count, with
+// its first logits on their way and all counts in flight at once, to 20.2 us; larger blocks, to 19.0.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -39,7 +40,6 @@ constexpr int kCountCtas = 8;
 constexpr int kCountThreads = 1024;
 constexpr int kCountUnroll = 4;
 constexpr int kCountIds = 8192, kMaxCounts = 16;
-constexpr int kLossThreads = 256;
 
 // Scratch of one call (device): sums [E] u64, the clusters' counts [n][E] and tokens [n], and
 // the ticket.
@@ -162,7 +162,7 @@ __device__ __forceinline__ int expert_of(int ti, int j) {
   return kVec ? 4 * (ti + j / 4 * kTeam) + j % 4 : ti + j * kTeam;
 }
 
-template <int kTeam, int kEpl, bool kVec, bool kSigmoid>
+template <int kTeam, int kEpl, bool kVec, bool kSigmoid, int kLossThreads>
 __global__ void __launch_bounds__(kLossThreads) balance_loss_kernel(const LossArgs a) {
   constexpr int kTeams = kLossThreads / kTeam;
   extern __shared__ float s_f[];  // f [E]; then [kTeams][E] sums
@@ -323,27 +323,45 @@ __global__ void __launch_bounds__(kLossThreads) balance_loss_kernel(const LossAr
   }
   __shared__ double s_sum[kLossThreads];
   s_sum[threadIdx.x] = part;
-  for (int w = kLossThreads / 2; w > 0; w >>= 1) {
+  for (int w = 512; w > 0; w >>= 1) {
     __syncthreads();
-    if (threadIdx.x < w) s_sum[threadIdx.x] += s_sum[threadIdx.x + w];
+    if (threadIdx.x < w && threadIdx.x + w < kLossThreads) s_sum[threadIdx.x] += s_sum[threadIdx.x + w];
   }
   if (threadIdx.x == 0 && a.loss != nullptr)
     a.loss[0] = (float)((double)a.alpha * E * s_sum[0]);
 }
 
+template <int kTeam, int kEpl, bool kVec, bool kSigmoid, int kThreads>
+cudaError_t launch_blocks(const LossArgs& a, int64_t blocks, cudaStream_t stream) {
+  const size_t smem = sizeof(float) * a.E * (1 + (a.want_sums ? kThreads / kTeam : 1));
+  return launch_pdl(balance_loss_kernel<kTeam, kEpl, kVec, kSigmoid, kThreads>, (unsigned)blocks,
+                    kThreads, smem, stream, a);
+}
+
+template <int kTeam, int kEpl, bool kVec, bool kSigmoid>
+cudaError_t launch_teams(const LossArgs& a, int sms, cudaStream_t stream) {
+  // blocks of 256 threads that the registers let be on an SM at once
+  constexpr int kPerSm = kEpl <= 2 ? 6 : kEpl == 4 ? 5 : kEpl == 8 ? (kSigmoid ? 3 : 4)
+                       : kEpl == 12 ? (kSigmoid ? 2 : 3) : kEpl == 16 ? 2 : 1;
+  const int64_t want = (a.N + 256 / kTeam - 1) / (256 / kTeam);
+  const int64_t most = kPerSm * (int64_t)sms;
+  // Many experts and tokens for all SMs: the same threads in one or two blocks on an SM, which read
+  // the counts and add up their sums once (16384 tokens of 384 experts: 19.0 us, 20.2 us in blocks
+  // of 256).
+  if constexpr (kEpl >= 8 && kEpl <= 16)
+    if (want > most) {
+      constexpr int kBlocks = kPerSm == 4 ? 2 : 1;
+      return launch_blocks<kTeam, kEpl, kVec, kSigmoid, 256 * kPerSm / kBlocks>(a, kBlocks * sms,
+                                                                                stream);
+    }
+  return launch_blocks<kTeam, kEpl, kVec, kSigmoid, 256>(
+      a, want < 1 ? 1 : want < most ? want : most, stream);
+}
+
 template <int kTeam, int kEpl, bool kVec>
 cudaError_t launch_rows(const LossArgs& a, bool sigmoid, int sms, cudaStream_t stream) {
-  constexpr int kTeams = kLossThreads / kTeam;
-  const size_t smem = sizeof(float) * a.E * (1 + (a.want_sums ? kTeams : 1));
-  const int64_t want = (a.N + kTeams - 1) / kTeams;
-  // blocks that the registers let be on an SM at once
-  const int per_sm = kEpl <= 2 ? 6 : kEpl == 4 ? 5 : kEpl == 8 ? (sigmoid ? 3 : 4)
-                   : kEpl == 12 ? (sigmoid ? 2 : 3) : kEpl == 16 ? 2 : 1;
-  const int grid = (int)(want < 1 ? 1 : want < per_sm * sms ? want : per_sm * sms);
-  return sigmoid ? launch_pdl(balance_loss_kernel<kTeam, kEpl, kVec, true>, grid, kLossThreads,
-                              smem, stream, a)
-                 : launch_pdl(balance_loss_kernel<kTeam, kEpl, kVec, false>, grid, kLossThreads,
-                              smem, stream, a);
+  return sigmoid ? launch_teams<kTeam, kEpl, kVec, true>(a, sms, stream)
+                 : launch_teams<kTeam, kEpl, kVec, false>(a, sms, stream);
 }
 
 // More than 64 experts: 16 bytes at a time where rows start on 16 bytes.

@@ -224,3 +224,43 @@ def test_graph_replay_and_side_stream():
     s.synchronize()
     for n in want:
         assert torch.equal(other[n], want[n]), n
+
+
+@pytest.mark.parametrize("score", [W.SOFTMAX, W.SIGMOID])
+@pytest.mark.parametrize("N,E,k", [(5001, 256, 8), (4999, 250, 2), (3601, 384, 6), (3700, 383, 1), (2500, 512, 4),
+                                   (2501, 509, 3)])
+def test_more_tokens_than_the_gpu_holds(N, E, k, score):
+    z, ids, mask = make(N, E, k, seed=N + E, masked=True)
+    out, _, ws = call(z, ids, mask, score)
+    check(out, z, ids, mask, score)
+    check_status(ws)
+    again, _, _ = call(z, ids, mask, score)
+    assert all(torch.equal(out[n], again[n]) for n in ("loss", "counts", "P", "dlogits"))
+
+
+def test_logits_written_just_before_the_call():
+    # (the row pass loads its first logits while the assignments are still being counted)
+    sets = [make(4000, 64, 2, seed=s, masked=False) for s in (1, 2)]
+    want = [call(z, ids, None, W.SOFTMAX)[0] for z, ids, _ in sets]
+    zs, idss = [dev(z) for z, _, _ in sets], [dev(i) for _, i, _ in sets]
+    z, ids = torch.empty_like(zs[0]), torch.empty_like(idss[0])
+    cfg = nat.make_config(4000, 8, 64, 2, 8)
+    ws = nat.alloc_workspace(cfg)
+    got = [dict(loss=torch.zeros(1, device="cuda"), dlogits=torch.zeros_like(z)) for _ in range(40)]
+    def run():
+        for i, g in enumerate(got):
+            z.copy_(zs[i % 2])
+            ids.copy_(idss[i % 2])
+            nat.moe_balance_loss(cfg, logits=z, ids=ids, alpha=0.01, ws=ws, **g)
+    def right():
+        torch.cuda.synchronize()
+        return all(torch.equal(g[n], want[i % 2][n]) for i, g in enumerate(got) for n in g)
+    run()
+    assert right()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for g in got:
+        g["dlogits"].zero_()
+    graph.replay()
+    assert right()
