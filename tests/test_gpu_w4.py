@@ -553,3 +553,32 @@ def test_layer_on_another_stream_takes_its_own_memory():
     torch.cuda.synchronize()
     assert not places & {g.data_ptr() for g in (got, got_total, got_plain)}
     assert torch.equal(got, want) and torch.equal(got_total, total) and torch.equal(got_plain, plain)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,rows,cols,parts", [
+    (16, 7176, 1288, 2), (3, 1544, 5128, 2),                            # clusters of 3
+    (3, 520, 7176, 1),                                                  # 4
+    (7, 2568, 7176, 2), (3, 1032, 14344, 2),                            # 5
+    (16, 4104, 5128, 2), (7, 1544, 5128, 2), (3, 520, 5128, 1),         # 6
+    (16, 3592, 5128, 2),                                                # 7
+    (3, 520, 14344, 1), (31, 7176, 1288, 2)])                           # 8; 2
+def test_clusters_of_every_size(n, rows, cols, parts, kind):
+    test_large_shapes(n, rows, cols, parts, 64, kind)
+
+
+@pytest.mark.parametrize("sizes", [[20, 3, 40, 0, 16, 17, 1, 8, 9, 33] * 5, [16] * 40 + [1] * 60, [5] * 30 + [31] * 20])
+def test_costly_and_cheap_tiles_in_rounds(sizes):
+    # more items than blocks: every row of every group still has its own expert's outputs
+    E, cols, rows, n = len(sizes), 264, 1032, sum(sizes)
+    w, wv = make_w(E, 1, rows, cols, 64, seed=E)
+    x, xs, xg, xv = make_x(n, cols, "bf16", seed=n)
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    out = torch.full((n + 2, rows), 7.0, device="cuda")
+    nat.moe_w4_matmul(w, x=torch.cat([x, x[:2]]), offsets=dev(off), out=out)
+    assert bool((out[n:] == 7.0).all())
+    got = f64(out)
+    for e in range(E):
+        a, b = off[e], off[e + 1]
+        v, tol = expect(wv[e], xv[a:b], cols, 64)
+        assert within(got[a:b], v, tol + np.abs(v) * 2.0 ** -24 + 1e-37), e
