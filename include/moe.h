@@ -107,7 +107,9 @@ typedef struct {
 } moe_route_out;
 
 /* Bytes of device workspace a call with this configuration needs (0 on a bad config).
- * The size depends on N, d, E, k, F, n_shared, n_bias_sets and dtype only. */
+ * The size depends on N, d, E, k, F, n_shared, n_bias_sets, dtype and, through the padded
+ * layout's E * capacity rows, capacity only.  It never falls as N or capacity grows: a workspace
+ * made for the largest batch serves every smaller one. */
 MOE_API size_t moe_workspace_size(const moe_config* cfg);
 
 /* Zero the workspace header (the device status word and the dispatch scan's ticket

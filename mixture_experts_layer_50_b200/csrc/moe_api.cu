@@ -87,6 +87,7 @@ size_t el_size(const moe_config& c) { return c.dtype == MOE_DT_BF16 ? 2 : 4; }
 // Router split-K: at most this many K slices.
 constexpr int kMaxLogitSplits = 16;
 int router_splits(const moe_config& c);
+size_t logit_part_rows(const moe_config& c);
 
 // Rows of the padded dispatch buffer [E][C] (0 without a capacity).
 int64_t padded_rows(const moe_config& c) { return c.capacity > 0 ? (int64_t)c.E * c.capacity : 0; }
@@ -126,8 +127,7 @@ Ws layout(const moe_config& c) {
   w.y_stage2 = take(N * d * el);
   w.balance = take(moe::balance_scratch_bytes((int64_t)N, (int)E, std::max(1, c.n_bias_sets)));
   w.offsets_pad = take((E + 1) * 4);
-  const int splits = router_splits(c);
-  w.logit_parts = take(splits > 1 ? (size_t)splits * N * E * 4 : 0);
+  w.logit_parts = take(logit_part_rows(c) * E * 4);
   // overflow policy "report": next-best candidates, their gate values, the first pass
   w.rr_cand = take(Nk * 4);
   w.rr_val = take(2 * Nk * 4);
@@ -260,6 +260,19 @@ int router_splits(const moe_config& c) {
   int splits = (int)std::min<int64_t>({want, (int64_t)kMaxLogitSplits, (int64_t)nk});
   const int per = (nk + splits - 1) / splits;
   return (nk + per - 1) / per;  // no empty slice
+}
+
+// Rows of partial logits that the workspace has room for: at least router_splits * n of any
+// batch of n <= N tokens.  Fewer tokens are cut into more slices, which may take more room than
+// the tokens themselves save, and a workspace of N tokens has to serve them too.  With t column
+// tiles and m token tiles, splits <= 128 / (m t), and n <= 128 m: no batch has more than
+// 128 * 128 / t rows; nor more than the most slices for each of its tokens.
+size_t logit_part_rows(const moe_config& c) {
+  const int bn = moe::router_tile_n(c.E);
+  const int64_t cols = (c.E + bn - 1) / bn;
+  const int64_t most = std::min(kMaxLogitSplits, (c.d + 63) / 64);
+  if (c.dtype != MOE_DT_BF16 || c.N == 0 || most < 2 || 128 / cols < 2) return 0;
+  return (size_t)std::min<int64_t>(most * c.N, 128 * 128 / cols);
 }
 
 moe_status stage_logits(const moe_config& c, const Ws& L, void* ws, const void* x,
