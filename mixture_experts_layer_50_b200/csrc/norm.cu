@@ -18,7 +18,7 @@
 // The sum of squares needs the whole row before its first output, so a row stays with one team of
 // threads that can hold it: a warp up to 128 vectors (eight rows in a block, no barrier), a block
 // beyond.  Two vectors a thread up to 512 of them and four beyond keep several blocks on an SM
-// (56 registers), whose loads cover one another's reductions; a few rows cannot fill the GPU and
+// (59 registers), whose loads cover one another's reductions; a few rows cannot fill the GPU and
 // take a vector a thread instead, which is the shortest way through a row.
 #include <cuda_fp8.h>
 
@@ -108,6 +108,7 @@ struct NormArgs {
   int64_t N;
   int d;
   float eps;
+  float low;  // a sum of squares below it is taken again, scaled (0: none is)
   int group;  // 128, or 0: one scale for a row
 };
 
@@ -164,14 +165,36 @@ __global__ void __launch_bounds__(kTeam == 32 ? 256 : 1024) rms_norm_kernel(cons
     }
   }
   __shared__ float s_part[32];
-  sq = warp_sum(sq);
-  if (kTeam != 32) {
-    if (lane == 0) s_part[warp] = sq;
-    __syncthreads();
-    const int nw = blockDim.x >> 5;
-    sq = warp_sum(lane < nw ? s_part[lane] : 0.f);
+  auto team_sum = [&](float v) {
+    v = warp_sum(v);
+    if (kTeam != 32) {
+      if (lane == 0) s_part[warp] = v;
+      __syncthreads();
+      const int nw = blockDim.x >> 5;
+      v = warp_sum(lane < nw ? s_part[lane] : 0.f);
+    }
+    return v;
+  };
+  sq = team_sum(sq);
+  float eps = a.eps;
+  // A row whose squares overflow, or vanish beside an eps that does too, is scaled by a power of
+  // two first: y stays the same.  2^-75 brings the largest sum (2^15 squares of 2^128) to 2^121,
+  // 2^100 the smallest number's square to 2^-98.
+  if (__builtin_expect(sq == INFINITY || sq < a.low, 0)) {
+    const float by = sq == INFINITY ? 0x1p-75f : 0x1p100f;
+    sq = 0.f;
+#pragma unroll
+    for (int i = 0; i < kVpt; ++i)
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        s[i][j] *= by;
+        sq = fmaf(s[i][j], s[i][j], sq);
+      }
+    eps = eps * by * by;
+    if (kTeam != 32) __syncthreads();  // the first sum's parts have been read
+    sq = team_sum(sq);
   }
-  const float r = rsqrtf(sq / (float)a.d + a.eps);
+  const float r = rsqrtf(sq / (float)a.d + eps);
   float rowmax = 0.f;
 #pragma unroll
   for (int i = 0; i < kVpt; ++i) {
@@ -258,7 +281,7 @@ cudaError_t launch_rms_norm(int64_t N, int d, bool f32, const void* x, const voi
                             float* y8_scale, int group, cudaStream_t stream, int* launches) {
   if (N == 0) return cudaSuccess;
   const NormArgs a{x, residual, weight, y, residual_out, static_cast<uint8_t*>(y8), y8_scale,
-                   N, d, eps, group};
+                   N, d, eps, eps < 0x1p-80f ? 0x1p-100f : 0.f, group};
   ++*launches;
   return f32 ? launch<float>(a, stream) : launch<__nv_bfloat16>(a, stream);
 }
