@@ -349,7 +349,7 @@ MOE_API moe_status moe_w4_quantize(const moe_w4* w, const void* W, moe_stream_t 
 
 /* out[r] = W_e x[r] for the rows r of each group (parts = 1), or SiLU(clamp(gate_e x[r])) *
  * clamp(up_e x[r]) (parts = 2).  Products are exact and sums are fp32; out is rounded once.
- * The sums of a row keep their full accuracy while its largest products are above 2^-57; bf16
+ * The sums of a row keep their full accuracy while its largest products are above 2^-58; bf16
  * values of 2^63 and more count as infinite, and a NaN or infinity makes its row's outputs NaN.
  *   x        bf16 [x_rows][cols], or with x_scale e4m3 [x_rows][cols]: x_scale fp32
  *            [x_rows][ceil(cols / 128)] (x_group = 128) or [x_rows][1] (x_group = 0), the two

@@ -18,7 +18,7 @@
 // g + 8.  The 8 that every code is too large by is -8 sum(x) over a group of columns, the same for
 // all weights: it is made once, where the rows arrive, and is what the group's sums start from.
 // The powers of two go into the result at the end.  To keep bf16 products out of fp32's own
-// subnormal range, the rows are multiplied by 2^64 as they arrive in shared memory; so a row's
+// subnormal range, the rows are multiplied by 2^65 as they arrive in shared memory; so a row's
 // numbers count as infinite from 2^63 on.  8-bit rows (e4m3 with scales) become fp16 there, and
 // their scales join the weights' scales on the sums.  All products are exact in the fp32
 // accumulators; a group's sum is multiplied by its scale in fp32, and nothing is rounded below 32
@@ -134,7 +134,9 @@ __device__ __forceinline__ void copy_x(uint32_t slot, const void* src) {
   else
     copy16(slot, src);
 }
-// The slot's eight columns as operands: bf16 times 2^64, or fp16; returns their sum.
+// The slot's eight columns as operands: bf16 times 2^65, or fp16; returns the sum of the columns
+// themselves (each is scaled back before it is added: 128 operands of one sign may add up to more
+// than fp32 holds), infinite or NaN where an operand is.
 template <bool kX8>
 __device__ __forceinline__ float make_x(uint32_t slot) {
   uint32_t v[4];
@@ -150,7 +152,7 @@ __device__ __forceinline__ float make_x(uint32_t slot) {
       sum += f.x + f.y;
     }
   } else {
-    const __nv_bfloat162 k = __floats2bfloat162_rn(18446744073709551616.f, 18446744073709551616.f);
+    const __nv_bfloat162 k = __floats2bfloat162_rn(0x1p65f, 0x1p65f);
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                  : "r"(slot)
@@ -159,7 +161,8 @@ __device__ __forceinline__ float make_x(uint32_t slot) {
     for (int i = 0; i < 4; ++i) {
       const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v[i]), k);
       v[i] = *reinterpret_cast<const uint32_t*>(&r);
-      sum += __uint_as_float(v[i] << 16) + __uint_as_float(v[i] & 0xffff0000u);
+      sum = fmaf(__uint_as_float(v[i] << 16), 0x1p-65f, sum);
+      sum = fmaf(__uint_as_float(v[i] & 0xffff0000u), 0x1p-65f, sum);
     }
   }
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(slot), "r"(v[0]), "r"(v[1]),
@@ -206,7 +209,7 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t (&a)[4]) {
 // What makes codes of them again, for rows g and rows g + 8.
 template <bool kX8>
 __device__ __forceinline__ float code_unit(bool upper) {
-  const float u = kX8 ? 16777216.f : 590295810358705651712.f;  // 2^24, 2^(133 - 64)
+  const float u = kX8 ? 0x1p24f : 0x1p68f;  // (133 - 65)
   return upper ? u * 0.0625f : u;
 }
 
@@ -472,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
         for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (i % kLanes == 0 && i < slots)
           asm volatile("st.shared.f32 [%0], %1;" ::"r"(sums + (i / kLanes * kTile + r) * 4),
-                       "f"(sum * (kX8 ? 1.f : 5.42101086e-20f) * (-8.f / code_unit<kX8>(false)))
+                       "f"(sum * (-8.f / code_unit<kX8>(false)))
                        : "memory");
       }
     }
