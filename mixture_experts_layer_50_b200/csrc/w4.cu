@@ -294,6 +294,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
       if constexpr (kNt > 1) mine += (int64_t)light << 32;
     }
     if (bad && blockIdx.x == 0) report_status(a.status, kStatusInvalidInput);
+    // (where offsets contradict each other, the last one does not bound the rows looked at above)
+    bad_index |= bad;
     if (threadIdx.x >= 1 && threadIdx.x <= kTile)
       s_x_steps[threadIdx.x] = x_steps_of(a.buf_bytes, kX8, kTile, threadIdx.x, kGroup);
     Count incl = mine;
