@@ -811,6 +811,10 @@ moe_status check_w4_size(const moe::W4Gemm& p) {
                         (p.shared_rows + 7) / 8;
   if (tiles * (p.rows / 256 + 1) > INT32_MAX / 32)
     return fail(MOE_ERR_UNSUPPORTED, "too many rows times outputs for one 4-bit product");
+  // nor may its tables of tiles run over where offsets contradict each other and every group has
+  // as many rows as one may have
+  if ((p.max_group_rows / 8 + 1) * p.n_groups + (p.shared_rows + 7) / 8 > INT32_MAX)
+    return fail(MOE_ERR_UNSUPPORTED, "too many rows times matrices for one 4-bit product");
   return MOE_OK;
 }
 
