@@ -7,6 +7,7 @@ raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from fractions import Fraction
@@ -190,6 +191,30 @@ def _stream(stream) -> Optional[int]:
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+def torch_stream(stream):
+    """``stream`` (None, a torch stream or a raw handle) as torch knows it: memory can be taken
+    from it and kept for it."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    if int(stream) in (0, 1):  # NULL and cudaStreamLegacy
+        return torch.cuda.default_stream()
+    return torch.cuda.ExternalStream(int(stream))
+
+
+def on_stream(stream):
+    """Memory taken inside belongs to ``stream`` (None: the current one): what the current stream
+    still does with memory that it has given back does not meet what ``stream`` writes."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def keep_for(stream, *tensors):
+    """The tensors' memory is not handed out again before ``stream`` is done with it."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
 
 
 def _check(st: int, where: str):
@@ -425,13 +450,18 @@ class W4Matrix:
             raise ValueError("parts must be 1 or 2 and divide W's rows; group 32, 64 or 128")
         rows = n // parts
         rb = -(-rows // 16)
-        q = torch.empty((mats, parts, rb, -(-cols // 64), 512), dtype=torch.uint8, device=W.device)
-        scale = torch.empty((mats, parts, rb, -(-cols // group), 8, 2), dtype=torch.bfloat16,
-                            device=W.device)
+        stream = torch_stream(stream)
+        with on_stream(stream):
+            q = torch.empty((mats, parts, rb, -(-cols // 64), 512), dtype=torch.uint8, device=W.device)
+            scale = torch.empty((mats, parts, rb, -(-cols // group), 8, 2), dtype=torch.bfloat16,
+                                device=W.device)
         w = cls(q, scale, rows=rows, cols=cols, group=group)
         st = lib.moe_w4_quantize(ctypes.byref(w.c), _typed(W, "W", torch.bfloat16, mats, n, cols),
                                  _stream(stream))
         _check(st, "moe_w4_quantize")
+        if stream is not None:
+            keep_for(stream, W)
+            keep_for(torch.cuda.current_stream(), q, scale)
         return w
 
 

@@ -1,7 +1,6 @@
 """MoELayer: a layer's device weights and workspace behind one ``forward`` call."""
 from __future__ import annotations
 
-import contextlib
 from typing import Optional
 
 import torch
@@ -140,14 +139,6 @@ class MoELayer:
         return nat.moe_check_status(self.ws, stream)
 
 
-def _on(stream):
-    """Memory taken inside belongs to ``stream``: what the current stream still does with memory
-    that it has given back does not meet what ``stream`` writes."""
-    if isinstance(stream, torch.cuda.Stream):
-        return torch.cuda.stream(stream)
-    return contextlib.nullcontext()
-
-
 class W4MoELayer(MoELayer):
     """A bf16 layer whose expert weights are held in 4 bits (``moe_forward_w4``), for decode.
 
@@ -191,13 +182,17 @@ class W4MoELayer(MoELayer):
                 stream=None, x8=None, x8_scale=None) -> torch.Tensor:
         N = x.shape[0]
         self._check_tokens(N)
+        stream = nat.torch_stream(stream)
         if y is None:
-            with _on(stream):
+            with nat.on_stream(stream):
                 y = torch.empty_like(x)
         nat.moe_forward_w4(self.config(N), x=x, x8=x8, x8_scale=x8_scale, W_g=self.W_g,
                            W_gu=self.W_gu, W_down=self.W_down, y=y,
                            logit_offset=self.logit_offset, bias=self.bias, modality=modality,
                            route_out=route_out, ws=self.ws, stream=stream)
+        if stream is not None:
+            nat.keep_for(stream, x, x8, x8_scale, modality, y, *(route_out or {}).values())
+            nat.keep_for(torch.cuda.current_stream(), y)
         return y
 
     def forward_normed(self, x: torch.Tensor, residual: torch.Tensor, weight=None,
@@ -205,7 +200,8 @@ class W4MoELayer(MoELayer):
                        stream=None):
         """The layer of RMS norm(x + residual) * weight; returns (y, x + residual)."""
         N, d = x.shape
-        with _on(stream):
+        stream = nat.torch_stream(stream)
+        with nat.on_stream(stream):
             h, total = torch.empty_like(x), torch.empty_like(x)
             h8 = torch.empty((N, d), dtype=torch.float8_e4m3fn, device=x.device)
             h8_scale = torch.empty((N, (d + 127) // 128), device=x.device)
@@ -213,18 +209,19 @@ class W4MoELayer(MoELayer):
                          y8=h8, y8_scale=h8_scale, stream=stream)
         y = self.forward(h, modality=modality, route_out=route_out, stream=stream, x8=h8,
                          x8_scale=h8_scale)
-        if isinstance(stream, torch.cuda.Stream):
-            for t in (x, residual):
-                t.record_stream(stream)
+        if stream is not None:
+            nat.keep_for(stream, x, residual, weight)
+            nat.keep_for(torch.cuda.current_stream(), total)
         return y, total
 
     def forward_host(self, x_host: torch.Tensor, y_host: torch.Tensor, modality=None,
                      stream=None) -> torch.Tensor:
         self._check_tokens(x_host.shape[0])
-        return self._forward_host_copies(x_host, y_host, modality, stream, sync=True)
+        return self._forward_host_copies(x_host, y_host, modality, nat.torch_stream(stream), sync=True)
 
     def forward_host_batches(self, x_host: list, y_host: list, modality=None, stream=None):
         self._check_tokens(x_host[0].shape[0])
+        stream = nat.torch_stream(stream)
         for xb, yb in zip(x_host, y_host):
             self._forward_host_copies(xb, yb, modality, stream, sync=False)
         (torch.cuda.current_stream() if stream is None else stream).synchronize()
