@@ -375,6 +375,20 @@ def _typed(t, name, dtype, *shape):
     return p
 
 
+def _room(t, name, n=0, *dtypes):
+    """Pointer of an optional tensor of the current device with room for n elements of a type."""
+    p = _ptr(t)
+    if t is None:
+        return p
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    if dtypes and t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, not {dtypes[0]}")
+    if t.numel() < n:
+        raise ValueError(f"{name} has {t.numel()} elements, not {n}")
+    return p
+
+
 _E4M3 = (torch.float8_e4m3fn, torch.uint8)
 
 
@@ -390,7 +404,7 @@ def moe_balance_loss(cfg, *, logits, ids, token_mask=None, alpha, grad_loss=None
         alpha, _typed(grad_loss, "grad_loss", torch.float32, 1),
         _typed(loss, "loss", torch.float32, 1), _typed(counts, "counts", torch.int32, E),
         _typed(P, "P", torch.float32, E), _typed(dlogits, "dlogits", torch.float32, N, E),
-        _ptr(ws), _stream(stream))
+        _room(ws, "ws"), _stream(stream))
     _check(st, "moe_balance_loss")
 
 
@@ -402,7 +416,7 @@ def moe_balance_loss_backward(cfg, *, logits, ids, token_mask=None, alpha, grad_
         ctypes.byref(cfg), _typed(logits, "logits", torch.float32, N, E),
         _typed(ids, "ids", torch.int32, N, k), _typed(token_mask, "token_mask", torch.uint8, N),
         alpha, _typed(grad_loss, "grad_loss", torch.float32, 1),
-        _typed(dlogits, "dlogits", torch.float32, N, E), int(accumulate), _ptr(ws),
+        _typed(dlogits, "dlogits", torch.float32, N, E), int(accumulate), _room(ws, "ws"),
         _stream(stream))
     _check(st, "moe_balance_loss_backward")
 
@@ -493,7 +507,7 @@ def moe_w4_matmul(w: W4Matrix, *, x, x_scale=None, x_group=128, offsets=None, ro
         _w4(w), px, ps, x_group, n, _typed(offsets, "offsets", torch.int32, w.mats + 1),
         _typed(row_index, "row_index", torch.int32, R), R, clamp,
         _typed(out, "out", (torch.bfloat16, torch.float32), R, w.rows),
-        F32 if out.dtype == torch.float32 else BF16, _ptr(ws), _stream(stream))
+        F32 if out.dtype == torch.float32 else BF16, _room(ws, "ws"), _stream(stream))
     _check(st, "moe_w4_matmul")
 
 
@@ -508,7 +522,7 @@ def moe_expert_ffn_w4(cfg, *, x, x_scale=None, offsets, row_token, W_gu: W4Matri
         ctypes.byref(cfg), px, ps, _typed(offsets, "offsets", torch.int32, cfg.E + 1),
         _typed(row_token, "row_token", torch.int32, nk), _w4(W_gu),
         _w4(W_down),
-        _typed(ye, "ye", torch.bfloat16, nk + cfg.n_shared * cfg.N, cfg.d), _ptr(ws),
+        _typed(ye, "ye", torch.bfloat16, nk + cfg.n_shared * cfg.N, cfg.d), _room(ws, "ws"),
         _stream(stream))
     _check(st, "moe_expert_ffn_w4")
 
@@ -520,14 +534,20 @@ def moe_forward_w4(cfg, *, x, x8=None, x8_scale=None, W_g, W_gu: W4Matrix, W_dow
     N, d = cfg.N, cfg.d
     ro = None
     if route_out:
-        ro = moe_route_out(*[_ptr(route_out.get(n)) for n, _ in moe_route_out._fields_])
+        sizes = dict(logits=N * cfg.E, ids=N * cfg.k, gates=N * cfg.k, counts=cfg.E, demand=cfg.E,
+                     drop_mask=N * cfg.k, offsets=cfg.E + 1)
+        types = dict(logits=(torch.float32,), gates=(torch.float32,), drop_mask=(torch.uint8, torch.bool))
+        ro = moe_route_out(*[_room(route_out.get(n), n, size, *types.get(n, (torch.int32,)))
+                             for n, size in sizes.items()])
     st = lib.moe_forward_w4(
         ctypes.byref(cfg), _typed(x, "x", torch.bfloat16, N, d), _typed(x8, "x8", _E4M3, N, d),
         _typed(x8_scale, "x8_scale", torch.float32, N, (d + 127) // 128),
-        _typed(W_g, "W_g", torch.bfloat16, cfg.E, d), _ptr(logit_offset), _ptr(bias),
-        _ptr(modality), _w4(W_gu), _w4(W_down),
+        _typed(W_g, "W_g", torch.bfloat16, cfg.E, d),
+        _room(logit_offset, "logit_offset", cfg.E, torch.float32),
+        _room(bias, "bias", cfg.n_bias_sets * cfg.E, torch.float32),
+        _room(modality, "modality", N, torch.uint8, torch.bool), _w4(W_gu), _w4(W_down),
         _typed(y, "y", torch.bfloat16, N, d), ctypes.byref(ro) if ro is not None else None,
-        _ptr(ws), _stream(stream))
+        _room(ws, "ws"), _stream(stream))
     _check(st, "moe_forward_w4")
 
 
