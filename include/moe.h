@@ -360,7 +360,8 @@ MOE_API moe_status moe_w4_quantize(const moe_w4* w, const void* W, moe_stream_t 
  *   rows     rows of out; those outside the groups are left untouched
  *   out      [rows][w->rows], out_dtype MOE_DT_BF16 or MOE_DT_F32
  *   ws       NULL, or a workspace whose status word records offsets or row indices out of range
- *            (MOE_ERR_INVALID_INPUT; such a group is skipped, such a row reads zeros)
+ *            (MOE_ERR_INVALID_INPUT; such a group is skipped, such a row reads zeros) and a
+ *            bounded wait that ran out (MOE_ERR_TIMEOUT; the outputs it concerns are NaN)
  * Meant for decode: weights are read once for every 16 rows of a group.  The result depends on
  * the inputs and sizes alone, not on the order of execution; the same row may give other last
  * bits in a batch of another size. */
@@ -624,6 +625,15 @@ MOE_API moe_status moe_forward_host_batches(const moe_config* cfg, int32_t n_bat
  * stays usable.  Asynchronous on `stream`; MOE_ERR_INVALID_ARG for a NULL ws or a limit
  * outside the range. */
 MOE_API moe_status moe_selftest_wait_timeout(void* ws, int64_t limit_ns, moe_stream_t stream);
+
+/* Self-test of the 4-bit products' bounded waits: moe_w4_matmul of one matrix, with the given warp
+ * of the grid (16 to a block) starting as if a wait of its own had run out.  The kernel ends
+ * normally and records MOE_ERR_TIMEOUT in ws (which may be NULL); every output that the warp's block
+ * has a part in is NaN, every other one is as always. */
+MOE_API moe_status moe_selftest_w4_give_up(const moe_w4* w, const void* x, const float* x_scale,
+                                           int32_t x_group, int64_t rows, void* out,
+                                           int32_t out_dtype, void* ws, int32_t warp,
+                                           moe_stream_t stream);
 
 /* Debugging aid (the pages have no counterpart): checks a dispatch layout's invariants on
  * the host -- ids in range and distinct within a token; offsets[0] = 0 and offsets[e+1] -

@@ -114,6 +114,7 @@ lib.moe_w4_size.argtypes = [_w4p, ctypes.POINTER(_sz)]
 lib.moe_w4_size.restype = _sz
 lib.moe_w4_quantize.argtypes = [_w4p, _vp, _vp]
 lib.moe_w4_matmul.argtypes = [_w4p, _vp, _vp, _i32, _i64, _vp, _vp, _i64, _f32, _vp, _i32, _vp, _vp]
+lib.moe_selftest_w4_give_up.argtypes = [_w4p, _vp, _vp, _i32, _i64, _vp, _i32, _vp, _i32, _vp]
 lib.moe_expert_ffn_w4.argtypes = [_cfgp] + [_vp] * 4 + [_w4p] * 2 + [_vp] * 3
 lib.moe_forward_w4.argtypes = [_cfgp] + [_vp] * 7 + [_w4p] * 2 + [_vp] * 4
 lib.moe_check_dispatch_host.argtypes = [_i64, _i32, _i32, _i64] + [_vp] * 8 + [_sz]
@@ -133,7 +134,7 @@ for _f in ("moe_workspace_init", "moe_route", "moe_permute", "moe_expert_ffn", "
            "moe_check_dispatch", "moe_ep_copy_runs", "moe_ipc_handle", "moe_ipc_open",
            "moe_ipc_close", "moe_permute_ep_p2p", "moe_ep_combine_p2p", "moe_balance_loss",
            "moe_balance_loss_backward", "moe_rms_norm", "moe_w4_quantize", "moe_w4_matmul",
-           "moe_expert_ffn_w4", "moe_forward_w4"):
+           "moe_expert_ffn_w4", "moe_forward_w4", "moe_selftest_w4_give_up"):
     getattr(lib, _f).restype = ctypes.c_int
 
 EXPORTED = ("moe_workspace_size", "moe_workspace_init", "moe_capacity", "moe_route",
@@ -148,7 +149,7 @@ EXPORTED = ("moe_workspace_size", "moe_workspace_init", "moe_capacity", "moe_rou
             "moe_ep_copy_runs", "moe_ipc_handle", "moe_ipc_open", "moe_ipc_close",
             "moe_permute_ep_p2p", "moe_ep_combine_p2p", "moe_balance_loss",
             "moe_balance_loss_backward", "moe_rms_norm", "moe_w4_size", "moe_w4_quantize",
-            "moe_w4_matmul", "moe_expert_ffn_w4", "moe_forward_w4")
+            "moe_w4_matmul", "moe_expert_ffn_w4", "moe_forward_w4", "moe_selftest_w4_give_up")
 
 
 def make_config(N, d, E, k, F, n_shared=0, n_bias_sets=0, score_fn=SOFTMAX, renorm=1,
@@ -509,6 +510,18 @@ def moe_w4_matmul(w: W4Matrix, *, x, x_scale=None, x_group=128, offsets=None, ro
         _typed(out, "out", (torch.bfloat16, torch.float32), R, w.rows),
         F32 if out.dtype == torch.float32 else BF16, _room(ws, "ws"), _stream(stream))
     _check(st, "moe_w4_matmul")
+
+
+def moe_selftest_w4_give_up(w: W4Matrix, *, x, x_scale=None, x_group=128, out, ws=None, warp, stream=None):
+    """moe_w4_matmul of one matrix with a warp of the grid that acts as if a wait had run out."""
+    n, d = x.shape
+    if d != w.cols:
+        raise ValueError(f"x has {d} columns, the weights {w.cols}")
+    px, ps = _row_scale(x, x_scale, x_group)
+    st = lib.moe_selftest_w4_give_up(
+        _w4(w), px, ps, x_group, n, _typed(out, "out", (torch.bfloat16, torch.float32), n, w.rows),
+        F32 if out.dtype == torch.float32 else BF16, _room(ws, "ws"), warp, _stream(stream))
+    _check(st, "moe_selftest_w4_give_up")
 
 
 def moe_expert_ffn_w4(cfg, *, x, x_scale=None, offsets, row_token, W_gu: W4Matrix,

@@ -154,6 +154,7 @@ struct W4Gemm {
   void* out;                 // [.][rows]
   int out_f32;
   int* status;
+  int give_up = -1;          // self-test: this warp of the grid acts as if a wait had run out
 };
 cudaError_t launch_w4(const W4Gemm& p, cudaStream_t stream, int* launches);
 cudaError_t launch_w4_quantize(const void* w, int64_t mats, int rows, int cols, int group, void* q,

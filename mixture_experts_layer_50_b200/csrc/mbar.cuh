@@ -39,6 +39,7 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
     if (*given_up) return false;
     if (global_timer_ns() - t0 > 2000000000ull || polls > 50000000u) {
       *given_up = 1;
+      __threadfence_block();  // before whatever the caller does without having waited
       report_status(status, kStatusTimeout);
       return false;
     }

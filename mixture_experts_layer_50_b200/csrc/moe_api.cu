@@ -866,6 +866,52 @@ moe_status stage_ffn_w4(const moe_config& c, const Ws& L, void* ws, const void* 
   return MOE_OK;
 }
 
+moe_status w4_matmul(const moe_w4* w, const void* x, const float* x_scale, int32_t x_group,
+                     int64_t x_rows, const int32_t* offsets, const int32_t* row_index,
+                     int64_t rows, float clamp, void* out, int32_t out_dtype, void* ws,
+                     moe_stream_t stream, int give_up) {
+  g_last_launches = 0;
+  MOE_TRY(check_w4(w, "w"));
+  if (rows < 0 || x_rows < 0) return fail(MOE_ERR_INVALID_ARG, "rows and x_rows must not be negative");
+  if (rows > (1 << 30) || x_rows > (1 << 30))
+    return fail(MOE_ERR_UNSUPPORTED, "more than 2^30 rows");
+  if (offsets == nullptr && w->mats != 1)
+    return fail(MOE_ERR_INVALID_ARG, "several matrices need offsets");
+  if (x_scale != nullptr && x_group != 0 && x_group != 128)
+    return fail(MOE_ERR_INVALID_ARG, "x_group must be 0 or 128");
+  if (row_index == nullptr && x_rows < rows)
+    return fail(MOE_ERR_INVALID_ARG, "x has fewer rows than out");
+  if (x_rows == 0 && rows > 0)  // (a row index out of range reads row 0 and drops it)
+    return fail(MOE_ERR_INVALID_ARG, "x has no rows");
+  if (!(clamp == clamp)) return fail(MOE_ERR_INVALID_ARG, "clamp is NaN");
+  if (out_dtype != MOE_DT_BF16 && out_dtype != MOE_DT_F32)
+    return fail(MOE_ERR_INVALID_ARG, "unknown out_dtype");
+  if (ws != nullptr) MOE_TRY(check_ws(nullptr, ws));
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(need(x, "x"));
+  MOE_TRY(need(out, "out"));
+  moe::W4Gemm p = w4_gemm(*w);
+  p.x = x;
+  p.x_scale = x_scale;
+  p.x_group = x_group;
+  p.x_rows = x_rows;
+  p.row_index = row_index;
+  p.offsets = offsets;
+  p.n_groups = w->mats;
+  p.max_rows = rows;
+  p.max_group_rows = rows;
+  p.clamp = clamp;
+  p.out = out;
+  p.out_f32 = out_dtype == MOE_DT_F32;
+  p.status = static_cast<int*>(ws);
+  p.give_up = give_up;
+  MOE_TRY(check_w4_size(p));
+  int launches = 0;
+  MOE_CUDA(moe::launch_w4(p, (cudaStream_t)stream, &launches), "4-bit product");
+  g_last_launches = launches;
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1305,45 +1351,16 @@ moe_status moe_w4_matmul(const moe_w4* w, const void* x, const float* x_scale, i
                          int64_t rows, float clamp, void* out, int32_t out_dtype, void* ws,
                          moe_stream_t stream) {
   NvtxRange nvtx_range("moe_w4_matmul");
-  g_last_launches = 0;
-  MOE_TRY(check_w4(w, "w"));
-  if (rows < 0 || x_rows < 0) return fail(MOE_ERR_INVALID_ARG, "rows and x_rows must not be negative");
-  if (rows > (1 << 30) || x_rows > (1 << 30))
-    return fail(MOE_ERR_UNSUPPORTED, "more than 2^30 rows");
-  if (offsets == nullptr && w->mats != 1)
-    return fail(MOE_ERR_INVALID_ARG, "several matrices need offsets");
-  if (x_scale != nullptr && x_group != 0 && x_group != 128)
-    return fail(MOE_ERR_INVALID_ARG, "x_group must be 0 or 128");
-  if (row_index == nullptr && x_rows < rows)
-    return fail(MOE_ERR_INVALID_ARG, "x has fewer rows than out");
-  if (x_rows == 0 && rows > 0)  // (a row index out of range reads row 0 and drops it)
-    return fail(MOE_ERR_INVALID_ARG, "x has no rows");
-  if (!(clamp == clamp)) return fail(MOE_ERR_INVALID_ARG, "clamp is NaN");
-  if (out_dtype != MOE_DT_BF16 && out_dtype != MOE_DT_F32)
-    return fail(MOE_ERR_INVALID_ARG, "unknown out_dtype");
-  if (ws != nullptr) MOE_TRY(check_ws(nullptr, ws));
-  if (rows == 0) return MOE_OK;
-  MOE_TRY(need(x, "x"));
-  MOE_TRY(need(out, "out"));
-  moe::W4Gemm p = w4_gemm(*w);
-  p.x = x;
-  p.x_scale = x_scale;
-  p.x_group = x_group;
-  p.x_rows = x_rows;
-  p.row_index = row_index;
-  p.offsets = offsets;
-  p.n_groups = w->mats;
-  p.max_rows = rows;
-  p.max_group_rows = rows;
-  p.clamp = clamp;
-  p.out = out;
-  p.out_f32 = out_dtype == MOE_DT_F32;
-  p.status = static_cast<int*>(ws);
-  MOE_TRY(check_w4_size(p));
-  int launches = 0;
-  MOE_CUDA(moe::launch_w4(p, (cudaStream_t)stream, &launches), "4-bit product");
-  g_last_launches = launches;
-  return MOE_OK;
+  return w4_matmul(w, x, x_scale, x_group, x_rows, offsets, row_index, rows, clamp, out, out_dtype,
+                   ws, stream, -1);
+}
+
+moe_status moe_selftest_w4_give_up(const moe_w4* w, const void* x, const float* x_scale,
+                                   int32_t x_group, int64_t rows, void* out, int32_t out_dtype,
+                                   void* ws, int32_t warp, moe_stream_t stream) {
+  if (warp < 0) return fail(MOE_ERR_INVALID_ARG, "warp must not be negative");
+  return w4_matmul(w, x, x_scale, x_group, rows, nullptr, nullptr, rows, 0.f, out, out_dtype, ws,
+                   stream, warp);
 }
 
 moe_status moe_expert_ffn_w4(const moe_config* cfg, const void* x, const float* x_scale,

@@ -79,6 +79,7 @@ struct Args {
   void* out;
   int out_f32;
   int* status;
+  int give_up;  // self-test: a warp of the grid that starts as if a wait had run out, or -1
 };
 
 // Warps of a block, as many as the registers allow (one block on an SM), and the steps of 256
@@ -407,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
   // of the two chunks copied last: rows, slots of a row, and those before the last column
   int d_rows[2] = {0, 0}, d_over[2] = {1, 1}, d_steps[2] = {0, 0};
   int d_slots[2] = {0, 0}, d_inside[2] = {0, 0};
-  bool dead = false;  // a wait ran out: nothing is stored any more
+  bool dead = false;  // a wait ran out
   auto copy_chunk = [&]() {
     if (c_it >= units) return;
     if (c_s == 0) {
@@ -552,6 +553,12 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
     copies_commit();
   };
 
+  if ((int)blockIdx.x * kWarps + warp == a.give_up) {
+    dead = true;
+    *(volatile int*)&s_abort = 1;
+    __threadfence_block();
+    report_status(a.status, kStatusTimeout);
+  }
   fetch_item();
   copy_chunk();
   fetch(0);
@@ -701,6 +708,18 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
       else
         steps(std::integral_constant<int, 2>{});
     }
+    // Where a wait of any of the block's warps has run out, rows may be missing or may have been
+    // overwritten under another warp: all that the block still stores or hands over is NaN, so that
+    // a caller without a status word learns of it too.
+    dead = __any_sync(0xffffffffu, dead || *(volatile int*)&s_abort != 0);
+    if (dead) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < kNt; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[m][n][i] = NAN;
+    }
     if (im.split > 1) {
       __syncthreads();  // the last unit's sums have been read
       // the warps but the first of each pair leave theirs
@@ -761,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
       }
       if (rank != 0) continue;
     }
-    if (dead || n_mine == 0 || ks != 0) continue;
+    if (n_mine == 0 || ks != 0) continue;
     // rows 16 b + g and + 8 of block b, and (without SwiGLU) of the block behind it
     const int row0 = 16 * (a.parts == 2 ? pair : 2 * pair) + g;
 #pragma unroll
@@ -951,6 +970,7 @@ cudaError_t launch_w4(const W4Gemm& p, cudaStream_t stream, int* launches) {
   a.out = p.out;
   a.out_f32 = p.out_f32;
   a.status = p.status;
+  a.give_up = p.give_up;
   // rows of a tile: enough for the largest group there can be, 16 at most
   const int64_t most = p.has_shared ? (p.shared_rows > p.max_group_rows ? p.shared_rows : p.max_group_rows)
                                     : p.max_group_rows;
