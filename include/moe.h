@@ -349,6 +349,9 @@ MOE_API moe_status moe_w4_quantize(const moe_w4* w, const void* W, moe_stream_t 
 
 /* out[r] = W_e x[r] for the rows r of each group (parts = 1), or SiLU(clamp(gate_e x[r])) *
  * clamp(up_e x[r]) (parts = 2).  Products are exact and sums are fp32; out is rounded once.
+ * The sums are of codes 0..15, from which 8 times the sum of x is taken: a sum's error goes with
+ * B = sum |x| scale, whatever the codes are, and is at most 2^-22 (26 group / 16 + 2 cols / group
+ * + 40) B; 2^-24 B was the most in rows of 4096 normal numbers.
  * The sums of a row keep their full accuracy while its largest products are above 2^-58; bf16
  * values of 2^63 and more count as infinite, and a NaN or infinity makes its row's outputs NaN.
  *   x        bf16 [x_rows][cols], or with x_scale e4m3 [x_rows][cols]: x_scale fp32
