@@ -243,6 +243,22 @@ struct LogitSrc {
   float* final_out;
 };
 
+// The grouped GEMM's tensor maps are encoded by the driver, which needs a context in the calling
+// thread; a thread whose first CUDA work this is has none until the runtime makes the device's
+// current.
+cudaError_t grouped_gemm(const moe::GroupedGemm& g, cudaStream_t st, int* launches,
+                         const char** why) {
+  thread_local bool bound = false;
+  if (!bound) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaSetDevice(dev);
+    if (e != cudaSuccess) return e;
+    bound = true;
+  }
+  return moe::launch_grouped_gemm(g, st, launches, why);
+}
+
 LogitSrc finished_logits(const float* z) { return LogitSrc{z, 1, 0, nullptr, nullptr}; }
 
 // Number of K slices for the router GEMM: a launch with few output tiles (few 128-token
@@ -319,7 +335,7 @@ moe_status stage_logits(const moe_config& c, const Ws& L, void* ws, const void* 
     *out = LogitSrc{parts, splits, c.N * (int64_t)c.E, logit_offset, logits};
   }
   const char* why = "router GEMM launch";
-  MOE_CUDA(moe::launch_grouped_gemm(g, st, launches, &why), why);
+  MOE_CUDA(grouped_gemm(g, st, launches, &why), why);
   prof_mark(st);
   return MOE_OK;
 }
@@ -536,7 +552,7 @@ moe_status stage_ffn(const moe_config& c, const Ws& L, void* ws, const void* xp,
   g1.max_group_rows = grp_max;
   if (routed_only) g1.has_shared = 0;  // the shared expert runs on the side stream
   const char* why = "gate/up GEMM launch";
-  MOE_CUDA(moe::launch_grouped_gemm(g1, st, launches, &why), why);
+  MOE_CUDA(grouped_gemm(g1, st, launches, &why), why);
   prof_mark(st);
 
   moe::GroupedGemm g2 = down_gemm(c, Nk, h, W_down, offsets, ye, status);
@@ -547,7 +563,7 @@ moe_status stage_ffn(const moe_config& c, const Ws& L, void* ws, const void* xp,
     g2.shared_out_row0 = 0;
   }
   why = "down GEMM launch";
-  MOE_CUDA(moe::launch_grouped_gemm(g2, st, launches, &why), why);
+  MOE_CUDA(grouped_gemm(g2, st, launches, &why), why);
   prof_mark(st);
   return MOE_OK;
 }
@@ -662,7 +678,7 @@ moe_status stage_shared_ffn(const moe_config& c, const Ws& L, void* ws, const vo
   g1.groups_b = 1;
   g1.max_rows_routed = 0;
   const char* why = "shared gate/up GEMM launch";
-  MOE_CUDA(moe::launch_grouped_gemm(g1, st, launches, &why), why);
+  MOE_CUDA(grouped_gemm(g1, st, launches, &why), why);
   moe::GroupedGemm g2 = down_gemm(c, Nk, h, W_down, nullptr, y, status);
   g2.n_routed = 0;
   g2.b = static_cast<const char*>(W_down) + (size_t)c.E * c.d * c.F * 2;
@@ -671,7 +687,7 @@ moe_status stage_shared_ffn(const moe_config& c, const Ws& L, void* ws, const vo
   g2.out_shared = y;
   g2.shared_out_row0 = 0;
   why = "shared down GEMM launch";
-  MOE_CUDA(moe::launch_grouped_gemm(g2, st, launches, &why), why);
+  MOE_CUDA(grouped_gemm(g2, st, launches, &why), why);
   return MOE_OK;
 }
 
