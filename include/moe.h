@@ -302,12 +302,12 @@ MOE_API moe_status moe_balance_loss_backward(const moe_config* cfg, const float*
  *   y8 [N][d] e4m3 bytes and y8_scale [N][ceil(d / 128)] (group = 128: every 128 columns, the
  *   last group may be shorter) or [N][1] (group = 0: one scale for a row), fp32
  * Any of y, residual_out and y8 with y8_scale may be NULL, but not all.  The norm takes the fp32
- * sum, not the stored one, and the 8-bit values the fp32 y; each output is rounded once.  A
- * group of zeros has scale 0; a scale is otherwise at least 2^-126.  A NaN or infinity in a
- * group makes its scale non-finite.  y may be x and residual_out may be residual (the same
- * buffer); no other overlap.  Rows whose squares leave fp32's range have the same y: any finite
- * sum is normed, however large, or small beside eps (0 included).  d a multiple of 8 (bf16, at most 32768) or 4 (fp32, at most
- * 16384); eps >= 0. */
+ * sum, not the stored one, and the 8-bit values the fp32 y; each output is rounded once (the
+ * quotient y / y8_scale is taken in fp32).  A group of zeros has scale 0; a scale is otherwise at
+ * least 2^-126.  A NaN or infinity in a group makes its scale non-finite.  y may be x and
+ * residual_out may be residual (the same buffer); no other overlap.  Rows whose squares leave
+ * fp32's range have the same y: any finite sum is normed, however large, or small beside eps (0
+ * included).  d a multiple of 8 (bf16, at most 32768) or 4 (fp32, at most 16384); eps >= 0. */
 MOE_API moe_status moe_rms_norm(int64_t N, int32_t d, int32_t dtype, const void* x,
                                 const void* residual, const void* weight, float eps, void* y,
                                 void* residual_out, void* y8, float* y8_scale, int32_t group,

@@ -21,7 +21,7 @@
 // Bound: one read of the logits and one write of the gradient; small batches by the two launches
 // (64 tokens of 256 experts and 8191 of 8 take 7.3 us each in a captured graph).  For 16384 padded
 // tokens of 384 experts the reads and writes are 7.8 us of 19.0: the count takes 5 us, its
-// additions and its cluster's meeting; in the row pass a scheduler issues in 42 % of its slots with 36 %
+// additions and its cluster's meeting; in the row pass a scheduler issues in 49 % of its slots with 38 %
 // of an SM's threads (80 registers hold twelve experts a lane, the next token's logits and the
 // sums of P), and warps wait for two or three reductions per token.  Reading a token ahead and 16
 // bytes at a time took the whole from 37.6 to 21.5 us; starting the row pass beside the count, with

@@ -3,7 +3,7 @@
 //
 //   s = x + residual                         (fp32; residual_out = s rounded to the row type)
 //   y = s * rsqrt(mean(s^2) + eps) * weight  (fp32; y rounded once to the row type)
-//   c = amax(|y| over a group) / 448,  y8 = e4m3(y / c)   (from the fp32 y, rounded once)
+//   c = amax(|y| over a group) / 448,  y8 = e4m3(y / c)   (from the fp32 y, times fp32's 1 / c)
 //
 // The norm takes the unrounded fp32 sum: only what is stored is rounded.  The reductions run in
 // fp32 over a fixed tree, so the result does not depend on the launch's timing.

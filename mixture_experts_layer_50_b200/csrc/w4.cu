@@ -23,15 +23,18 @@
 // their scales join the weights' scales on the sums.  All products are exact in the fp32
 // accumulators; a group's sum is multiplied by its scale in fp32, and nothing is rounded below 32
 // bits before the output.  (For one token at 4096 x 14336 x 2: 33 us with a subtraction for each
-// operand, 17.3 us with five instructions for a word, 16.2 us with four.  The fifth-generation
-// tensor cores would want the operands in shared memory first, at 16 bits a weight more than an
-// SM's shared memory moves at this rate; at these few rows mma.sync is 20 to 30 % busy.)
+// operand, 17.3 us with five instructions for a word, 16.2 us with four.  mma.sync takes the
+// operands from the registers that they are made in and is 20 to 32 % busy.  The fifth-generation
+// tensor cores take them from shared or tensor memory, so each decoded weight would be stored
+// first, at 16 bits; in return one decoding could serve all rows of a group, which here every tile
+// of 16 rows does again.  Not built: at up to 16 rows there is nothing to share.)
 //
 // A block of 16 warps, one on an SM, owns one tile of a group's rows (8 or 16) and 512 output
 // rows, each warp two blocks of 16 of them (for SwiGLU a gate block and its up block).  Every warp
 // runs a ring of its own in shared memory for the weights that it alone needs: each lane copies
 // asynchronously what that lane will read, kDepth steps of 256 columns ahead and on across items,
 // without a barrier (registers held no more than two steps of 128, and waited for one another).
+// 16 warps leave each thread 128 registers; tiles of 16 rows spill 16 to 80 bytes of them.
 // The activation rows, which all warps need, come in chunks of several steps into three buffers:
 // every warp copies its part of a chunk two chunks ahead and makes operands of it one chunk ahead,
 // and mbarriers tell when all have, so the warps may run apart by most of a chunk.
