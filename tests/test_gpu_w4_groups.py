@@ -49,3 +49,25 @@ def test_the_same_row_in_two_groups_of_decreasing_offsets():
         v, tol = expect(wv[e], xv, 128, 64)
         near.append(np.abs(got - v) <= tol + np.abs(v) * 2.0 ** -24)
     assert near[0][:10].all() and near[1][40:].all() and (near[0] | near[1])[10:40].all()
+
+
+@pytest.mark.parametrize("wrong", [[], [5, 6, 4000, 8989], [0, 4, 8990, 9000]])
+def test_more_row_indices_than_are_looked_over_at_the_start(wrong):
+    # beyond 8192 rows every tile looks at its own; indices outside the groups are nobody's
+    w, wv = make_w(2, 1, 64, 264, 64, seed=46)
+    x, _, _, xv = make_x(300, 264, "bf16", seed=47)
+    idx = np.random.default_rng(48).integers(0, 300, 9001).astype(np.int32)
+    idx[wrong] = 300
+    off = np.array([5, 4000, 8990], np.int32)
+    ws = torch.zeros(512, dtype=torch.uint8, device="cuda")
+    ws = ws[(-ws.data_ptr()) % 256:][:256]
+    out = torch.full((9001, 64), -3.0, device="cuda")
+    nat.moe_w4_matmul(w, x=x, offsets=dev(off), row_index=dev(idx), out=out, ws=ws)
+    inside = [r for r in wrong if 5 <= r < 8990]
+    assert nat.moe_check_status(ws) == (nat.MOE_ERR_INVALID_INPUT if inside else 0)
+    got = f64(out)
+    assert (got[inside] == 0).all() and (got[:5] == -3).all() and (got[8990:] == -3).all()
+    for e in range(2):
+        rows = np.setdiff1d(np.arange(off[e], off[e + 1]), np.array(inside, int))
+        v, tol = expect(wv[e], xv[idx[rows]], 264, 64)
+        assert (np.abs(got[rows] - v) <= tol + np.abs(v) * 2.0 ** -24).all()

@@ -144,3 +144,22 @@ def test_quantised_weights_given_back_while_the_other_stream_still_reads_them():
     assert not taken_anew({place}, side, lambda: torch.zeros_like(like))
     torch.cuda.synchronize()
     assert torch.equal(got.q, want.q) and torch.equal(got.scale, want.scale)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_captured_on_a_stream_that_is_given(raw):
+    w4, x = layer()
+    want, (want_n, total) = w4.forward(x), w4.forward_normed(x, x)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        stream = side.cuda_stream if raw else side
+        y = w4.forward(x, stream=stream)
+        n, t = w4.forward_normed(x, x, stream=stream)
+    for _ in range(2):
+        for o in (y, n, t):
+            o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(n, want_n) and torch.equal(t, total)
